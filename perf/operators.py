@@ -229,7 +229,7 @@ def _plain_plan_step(held, want, table, free, count, P, N):
     R = drop.sum()
     c0 = count.long()
     top = c0 + R
-    served = fits & (take.cumsum(0) <= top)
+    served = fits & ((take == 0) | (take.cumsum(0) <= top))
     granted = torch.where(served, want, held)
     col = torch.arange(mp, device=table.device)
     # released pages onto the list, the first on top
