@@ -236,7 +236,9 @@ moda_status moda_set_phase_events(void* const* events, int n);
 /*
  * Synchronises `stream`, then reads and clears the current device's kernel
  * status word.  MODA_ERR_TIMEOUT if a kernel's bounded wait ran out since the
- * last check, MODA_ERR_CUDA if the stream reports an error, else MODA_OK.
+ * last check, MODA_ERR_INVALID_ARG if a paged call met a length, page, slot or
+ * parent on the device that was out of range (each call says below what it
+ * then did), MODA_ERR_CUDA if the stream reports an error, else MODA_OK.
  */
 moda_status moda_check_status(moda_stream_t stream);
 
@@ -270,6 +272,139 @@ moda_status moda_decode(const moda_shape* shape, const void* q, const void* K, c
                         void* ws, size_t ws_bytes, moda_stream_t stream);
 
 /*
+ * Serving over a paged KV cache: requests of different lengths, several new
+ * tokens a request (drafts: a tree or a chain; a chunk of a prompt).  The
+ * pages have no counterpart; the attention is the operator above on the newest
+ * positions, with the causal mask replaced by "the held keys, and the new keys
+ * on the token's own branch".
+ *
+ * A step:  moda_page_plan makes room for the new tokens and says where each
+ * goes; moda_cache_append writes their keys and values there (once a layer);
+ * moda_tree_mask turns the drafted trees into mask rows and positions;
+ * moda_tree_decode attends (once a layer).  When a branch has been accepted,
+ * moda_cache_append writes its tokens' keys and values again at the positions
+ * they keep, and moda_page_plan with the accepted lengths gives pages back.
+ *
+ *   cache        [n_pages, Hk, page_size, d], one tensor for K and one for V
+ *   block_table  [B, max_pages] int32: entry j of request b is the page of its
+ *                keys [j*page_size, (j+1)*page_size)
+ *   slot         page * page_size + offset within the page
+ *   cu_new       [B+1] int32: request b's new tokens are rows cu_new[b] ..
+ *                cu_new[b+1]-1 of the token arrays, which have N rows; rows
+ *                from cu_new[B] on are padding: not read, and left as they
+ *                were (but for slot_map, which says -1 there)
+ *   held_len     [B] int32: keys of request b before its new tokens
+ * Lengths, tables and slots live on the device, so a captured graph can be
+ * replayed with others.  Conventions as at the top of this file; every pointer
+ * is 16-byte aligned.  What is out of range on the device is never followed:
+ * it is cut off or skipped as described below and reported by the next
+ * moda_check_status as MODA_ERR_INVALID_ARG.
+ */
+typedef struct moda_paged_shape {
+    int B;            /* requests, >= 0                                        */
+    int N;            /* rows of the token arrays, >= 0                        */
+    int Hq, Hk;       /* heads, as in moda_shape; G = Hq / Hk <= 64            */
+    int d;            /* 64 or 128                                             */
+    int L;            /* depth rows of a new token, >= 0                       */
+    int page_size;    /* tokens a page: a power of two in 8..1024              */
+    int n_pages;      /* pages of the cache, >= 1                              */
+    int max_pages;    /* columns of the block table, >= 1                      */
+    int mask_words;   /* 32-bit words of a mask row, 0..64; 0: no mask (chain) */
+    moda_dtype dtype; /* of q, caches, depth rows and o                        */
+    float softmax_scale;  /* >= 0 and finite; 0 selects 1/sqrt(d)              */
+    int depth_window; /* as in moda_shape                                      */
+} moda_paged_shape;
+/* moda_page_plan uses B, N and the page fields; moda_cache_append those and
+   Hk, d, dtype; moda_tree_mask B, N, the page fields and mask_words. */
+
+/*
+ * Pages and slots from lengths: request b holds held_len[b] tokens and is to
+ * hold want_len[b].  Where that needs more pages they are taken off the free
+ * list and entered in the block table; where it needs fewer, the pages behind
+ * are given back and their entries set to -1 (want_len = 0 ends a request).
+ *   held_len, want_len  [B]
+ *   block_table         [B, max_pages]  in and out
+ *   free_pages          [n_pages]       in and out: the free pages are the first
+ *   free_count          [1]             free_count entries (the last is on top;
+ *                                       entries from free_count on are left over)
+ *   cu_new              [B+1]  out: prefix sums of max(granted - held, 0)
+ *   granted_len         [B]    out: want_len, or held_len where the request was
+ *                              refused: it does not fit its row of the table, or
+ *                              it needs pages and the list (with the pages given
+ *                              back in this call) does not cover it and all
+ *                              requests before it.  A
+ *                              refused request is left as it was.
+ *   slot_map            [N] int64  out: the slot of each new token, -1 behind
+ * The list is a stack, and a call that gives back exactly what the last call
+ * took restores it.  held_len is not changed; granted_len is the next call's
+ * held_len, in a buffer of its own (it may alias neither length).  B <= 16384.  Deterministic.
+ * Out of range: lengths are cut to 0..max_pages*page_size; new tokens behind N
+ * get no slot; a free_count above n_pages counts as n_pages.
+ */
+moda_status moda_page_plan(const moda_paged_shape* shape, const int* held_len, const int* want_len,
+                           int* block_table, int* free_pages, int* free_count, int* cu_new,
+                           int* granted_len, long long* slot_map, moda_stream_t stream);
+
+/*
+ * Writes row i of k_new and v_new [N, Hk, d] into slot slot_map[i] of the
+ * caches; -1 skips the row.  Bytes are copied as they are.  The slots of one
+ * call must differ (which row a slot named twice holds is not defined), and
+ * the inputs must not overlap the caches.  Out of range: the row is skipped.
+ */
+moda_status moda_cache_append(const moda_paged_shape* shape, const void* k_new, const void* v_new,
+                              const long long* slot_map, void* k_cache, void* v_cache,
+                              moda_stream_t stream);
+
+/*
+ * Mask rows and positions of drafted trees.
+ *   parent    [N]  a token's parent: the index of an earlier token of its own
+ *                  request, counted from the request's first, or -1 for a child
+ *                  of the last held token
+ *   cu_new    [B+1];  held_len  [B] or NULL (0)
+ *   mask      [N, mask_words]  out: bit j of row i (bit j%32 of word j/32) is
+ *                  set iff j is i or an ancestor of i
+ *   position  [N]  out: held_len + the number of proper ancestors among the new
+ *                  tokens
+ * A request may have at most 32*mask_words new tokens.  Out of range: tokens
+ * behind those get no row, and a parent that is no earlier token counts as -1.
+ */
+moda_status moda_tree_mask(const moda_paged_shape* shape, const int* parent, const int* cu_new,
+                           const int* held_len, unsigned int* mask, int* position,
+                           moda_stream_t stream);
+
+/*
+ * Attention of the new tokens, whose keys and values are in the cache already
+ * (request b's new token j is key held_len[b] + j):  token i of request b sees
+ *   the keys 0 .. held_len[b]-1,
+ *   new key j iff bit j of its mask row is set; without a mask iff j <= i,
+ *   its own depth rows (the last depth_window of them),
+ * under one softmax scaled by softmax_scale.
+ *   q         [N, Hq, d]
+ *   k_cache, v_cache   block_table   held_len   cu_new   as above
+ *   Kd, Vd    [N, Hk, L, d]  the tokens' depth rows (NULL if L == 0)
+ *   mask      [N, mask_words], NULL iff mask_words == 0
+ *   o         [N, Hq, d]   out;  lse [N, Hq] float32  out, natural log
+ *   ws        moda_tree_decode_workspace_size(shape) bytes, overwritten; calls
+ *             that may overlap in time (other streams, other captured graphs)
+ *             need one each.  Ask for the size with the device that runs the
+ *             call current: it follows the SM count.
+ * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not
+ * see (keys behind the last new token, other branches, other tokens' depth
+ * rows) has no influence on it, whatever it holds, infinities and NaN included.
+ * Deterministic: no floating-point atomics.  bf16: scores and sums in fp32, the
+ * weights rounded to bf16 for the product with V.
+ * Out of range: lengths are cut to the table, to N and to 32*mask_words new
+ * tokens (rows behind those are not written), and a table entry that names no
+ * page reads as zeros.
+ */
+size_t moda_tree_decode_workspace_size(const moda_paged_shape* shape);
+moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const void* k_cache,
+                             const void* v_cache, const void* Kd, const void* Vd,
+                             const int* block_table, const int* held_len, const int* cu_new,
+                             const unsigned int* mask, void* o, float* lse, void* ws,
+                             size_t ws_bytes, moda_stream_t stream);
+
+/*
  * Failure-path self-test (the pages have no counterpart).  Queues on `stream`
  * one small kernel whose warps wait, through the same bounded mbarrier wait
  * the forward and backward kernels use, on a barrier that nothing arrives on.
@@ -288,7 +423,8 @@ const char* moda_status_string(moda_status status);
 const char* moda_last_error_message(void);
 
 /* Library version, major*10000 + minor*100 + patch. */
-int moda_version(void);   /* 10200: adds MODA_DEPTH_LAYER (10100: flags and depth_window in moda_shape) */
+int moda_version(void);   /* 10300: adds the paged calls (10200: MODA_DEPTH_LAYER; 10100: flags and
+                             depth_window in moda_shape) */
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -18,7 +18,9 @@ definitions it follows:
 * Paper summary, "Hardware-Efficient Implementation" (layer-major versus
   token-major depth layout, for the repack).
 
-``decode`` evaluates the newest token's rows through the same C row function.
+``decode`` evaluates the newest token's rows through the same C row function,
+and so does ``tree_decode`` for drafted tokens over a paged cache; ``page_plan``
+and ``tree_mask`` are plain loops.
 
 Parity status: the forward, backward and repack are pinned by the CPU tests
 (the pins live in ``tests/oracle_pins.py`` and run from ``tests/test_oracle.py``):
@@ -205,6 +207,91 @@ def decode(q, K, V, Kd=None, Vd=None, window: int = 0, scale: float = 0.0, lib=N
             o[b, h], lse[b, h] = row(q[b, h], K[b, hk], V[b, hk], Kd[b, hk, lo:], Vd[b, hk, lo:],
                                      scale=scale, lib=lib)
     return o, lse
+
+
+def tree_mask(parent, cu, held=None):
+    """Ancestor matrices and positions of drafted trees: a list of bool [n, n]
+    arrays (row i: i and its ancestors) and positions [cu[-1]]."""
+    see, pos = [], []
+    for b in range(len(cu) - 1):
+        n = int(cu[b + 1]) - int(cu[b])
+        m = np.zeros((n, n), dtype=bool)
+        for i in range(n):
+            p = int(parent[int(cu[b]) + i])
+            if p >= 0:
+                m[i] = m[p]
+            m[i, i] = True
+            pos.append((0 if held is None else int(held[b])) + int(m[i].sum()) - 1)
+        see.append(m)
+    return see, np.array(pos, dtype=np.int64)
+
+
+def tree_decode(q, kc, vc, Kd, Vd, table, held, cu, see=None, window: int = 0, scale: float = 0.0, lib=None):
+    """New tokens over a paged cache, a row at a time from exactly the rows it
+    sees.  q [N,Hq,d]; kc, vc [n_pages,Hk,P,d]; Kd, Vd [N,Hk,L,d] or None;
+    table [B,max_pages]; see: per request a bool [n, n] matrix (row i: the new
+    tokens that token i sees), None for chains.  Returns (o [N,Hq,d],
+    lse [N,Hq]) in float64; rows from cu[-1] on are NaN, a row that sees
+    nothing is 0 with lse -inf."""
+    q, kc, vc = _f64(q), _f64(kc), _f64(vc)
+    N, Hq, d = q.shape
+    Hk, P = kc.shape[1], kc.shape[2]
+    G = Hq // Hk
+    L = 0 if Kd is None or np.size(Kd) == 0 else Kd.shape[2]
+    Kd = _f64(Kd) if L else np.zeros((N, Hk, 0, d))
+    Vd = _f64(Vd) if L else np.zeros((N, Hk, 0, d))
+    lo = L - window if 0 < window < L else 0
+    o = np.full((N, Hq, d), np.nan)
+    lse = np.full((N, Hq), np.nan)
+    for b in range(len(held)):
+        h, c0, n = int(held[b]), int(cu[b]), int(cu[b + 1]) - int(cu[b])
+        key = np.arange(h + n)
+        page = np.asarray(table[b])[key // P].astype(np.int64)
+        for i in range(n):
+            mine = np.ones(h + n, dtype=bool)
+            mine[h:] = see[b][i] if see is not None else np.arange(n) <= i
+            for hq in range(Hq):
+                hk = hq // G
+                k = np.concatenate([kc[page[mine], hk, key[mine] % P], Kd[c0 + i, hk, lo:]])
+                if k.shape[0] == 0:
+                    o[c0 + i, hq], lse[c0 + i, hq] = 0.0, -np.inf
+                    continue
+                v = np.concatenate([vc[page[mine], hk, key[mine] % P], Vd[c0 + i, hk, lo:]])
+                o[c0 + i, hq], lse[c0 + i, hq] = row(q[c0 + i, hq], k, v, k[:0], v[:0], scale=scale, lib=lib)
+    return o, lse
+
+
+def page_plan(held, want, table, free, P: int, N: int):
+    """Pages and slots from lengths, request by request with a list as the
+    stack (last entry on top).  table is a list of lists of pages (only the
+    pages held).  Returns (cu, granted, slots [N], table, free)."""
+    max_pages = table["max_pages"]
+    rows = [list(r) for r in table["rows"]]
+    free = list(free)
+    n_of = lambda x: (int(x) + P - 1) // P  # noqa: E731
+    released = []
+    for b in range(len(held)):
+        if n_of(want[b]) <= max_pages:
+            released += rows[b][n_of(want[b]):n_of(held[b])]
+            del rows[b][n_of(want[b]):]
+    free += released[::-1]                      # the first request's first page on top
+    granted, asked, top = [], 0, len(free)
+    for b in range(len(held)):
+        take = n_of(want[b]) - n_of(held[b]) if n_of(want[b]) <= max_pages else 0
+        take = max(take, 0)
+        asked += take
+        if n_of(want[b]) > max_pages or (take > 0 and asked > top):
+            granted.append(int(held[b]))
+            continue
+        rows[b] += [free.pop() for _ in range(take)]
+        granted.append(int(want[b]))
+    cu, slots = [0], []
+    for b in range(len(held)):
+        for key in range(int(held[b]), granted[b]):
+            slots.append(rows[b][key // P] * P + key % P)
+        cu.append(len(slots))
+    slots = (slots + [-1] * N)[:N]
+    return cu, granted, slots, rows, free
 
 
 def repack(src, B: int, Hk: int, T: int, d: int, L: int, lib=None) -> np.ndarray:

@@ -33,6 +33,8 @@ MODA_FLAG_NONCAUSAL = 1
 # Every symbol include/moda.h declares.
 EXPORTED = ("moda_workspace_size", "moda_repack_depth", "moda_fwd", "moda_bwd",
             "moda_bwd_noalloc", "moda_decode", "moda_decode_workspace_size",
+            "moda_page_plan", "moda_cache_append", "moda_tree_mask", "moda_tree_decode",
+            "moda_tree_decode_workspace_size",
             "moda_set_phase_events", "moda_check_status",
             "moda_selftest_wait_timeout", "moda_status_string", "moda_last_error_message",
             "moda_version")
@@ -44,6 +46,13 @@ class moda_shape(ctypes.Structure):
                 ("C", ctypes.c_int), ("dtype", ctypes.c_int), ("depth_layout", ctypes.c_int),
                 ("softmax_scale", ctypes.c_float), ("flags", ctypes.c_int),
                 ("depth_window", ctypes.c_int)]
+
+
+class moda_paged_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int), ("L", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("mask_words", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("softmax_scale", ctypes.c_float), ("depth_window", ctypes.c_int)]
 
 
 class MoDAError(RuntimeError):
@@ -85,6 +94,17 @@ def load(path: Optional[str] = None):
         lib.moda_decode_workspace_size.restype = sz
         lib.moda_decode.argtypes = [sp] + [vp] * 7 + [vp, sz, vp]
         lib.moda_decode.restype = i
+        pp = ctypes.POINTER(moda_paged_shape)
+        lib.moda_page_plan.argtypes = [pp] + [vp] * 8 + [vp]
+        lib.moda_page_plan.restype = i
+        lib.moda_cache_append.argtypes = [pp] + [vp] * 5 + [vp]
+        lib.moda_cache_append.restype = i
+        lib.moda_tree_mask.argtypes = [pp] + [vp] * 5 + [vp]
+        lib.moda_tree_mask.restype = i
+        lib.moda_tree_decode_workspace_size.argtypes = [pp]
+        lib.moda_tree_decode_workspace_size.restype = sz
+        lib.moda_tree_decode.argtypes = [pp] + [vp] * 11 + [vp, sz, vp]
+        lib.moda_tree_decode.restype = i
         lib.moda_set_phase_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i]
         lib.moda_set_phase_events.restype = i
         lib.moda_check_status.argtypes = [vp]
@@ -113,6 +133,16 @@ def make_shape(B, Hq, Hk, T, d, L, C=0, dtype=MODA_BF16, depth_layout=MODA_DEPTH
                softmax_scale=0.0, flags=0, depth_window=0) -> moda_shape:
     return moda_shape(int(B), int(Hq), int(Hk), int(T), int(d), int(L), int(C), int(dtype),
                       int(depth_layout), float(softmax_scale), int(flags), int(depth_window))
+
+
+def make_paged_shape(B, N, Hq, Hk, d, L, page_size, n_pages, max_pages, mask_words=0, dtype=MODA_BF16,
+                     softmax_scale=0.0, depth_window=0) -> moda_paged_shape:
+    """Sizes of a batch over a paged cache: B requests, N new-token rows,
+    pages of page_size tokens, max_pages block-table columns, mask_words
+    32-bit words a mask row (0: chains, no mask)."""
+    return moda_paged_shape(int(B), int(N), int(Hq), int(Hk), int(d), int(L), int(page_size), int(n_pages),
+                            int(max_pages), int(mask_words), int(dtype), float(softmax_scale),
+                            int(depth_window))
 
 
 def _ptr(x) -> Optional[int]:
@@ -272,6 +302,104 @@ def moda_decode(shape: moda_shape, q, K, V, Kd, Vd, o, lse, ws, ws_bytes: int, s
     _check(load().moda_decode(ctypes.byref(shape), _ptr(q), _ptr(K), _ptr(V), _ptr(Kd), _ptr(Vd),
                               _ptr(o), _ptr(lse), _ptr(ws), int(ws_bytes), _stream(stream)),
            "moda_decode")
+
+
+def _paged_args(where: str, specs):
+    """Addresses of the arguments of a paged call, checked as `_expect` and
+    `_ptr` check the others; a spec is (name, tensor or int or None, least
+    element count, dtype).  Kept short: these calls run once a layer of every
+    decoding step, where the host's time counts."""
+    import torch
+    for name, x, count, dtype in specs:
+        if x is None or isinstance(x, int):
+            continue
+        if x.dtype is not dtype:
+            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} has dtype {x.dtype}, expected {dtype}")
+        if x.numel() < count:
+            raise MoDAError(MODA_ERR_INVALID_ARG, where,
+                            f"{name} holds {x.numel()} elements, the shape needs {count}")
+    out, dev = [], None
+    for name, x, _, _ in specs:
+        if x is None or isinstance(x, int):
+            out.append(x)
+            continue
+        if not x.is_cuda:
+            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} is on {x.device}, not a CUDA device")
+        if not x.is_contiguous():
+            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} is not contiguous (row-major)")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if x.get_device() != dev:
+            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} is on {x.device}, current device is cuda:{dev}")
+        out.append(x.data_ptr())
+    return out
+
+
+def _paged_dtype(shape: moda_paged_shape):
+    import torch
+    return torch.float32 if shape.dtype == MODA_FP32 else torch.bfloat16
+
+
+def moda_page_plan(shape: moda_paged_shape, held_len, want_len, block_table, free_pages, free_count, cu_new,
+                   granted_len, slot_map, stream=None):
+    """Make room for want_len tokens a request (or give pages back): updates
+    block_table, free_pages and free_count, writes cu_new, granted_len and
+    slot_map."""
+    import torch
+    B, i32 = max(0, shape.B), torch.int32
+    args = _paged_args("moda_page_plan", (
+        ("held_len", held_len, B, i32), ("want_len", want_len, B, i32),
+        ("block_table", block_table, B * shape.max_pages, i32), ("free_pages", free_pages, shape.n_pages, i32),
+        ("free_count", free_count, 1, i32), ("cu_new", cu_new, B + 1, i32), ("granted_len", granted_len, B, i32),
+        ("slot_map", slot_map, shape.N, torch.int64)))
+    _check(load().moda_page_plan(ctypes.byref(shape), *args, _stream(stream)), "moda_page_plan")
+
+
+def moda_cache_append(shape: moda_paged_shape, k_new, v_new, slot_map, k_cache, v_cache, stream=None):
+    """Write the rows of k_new and v_new [N, Hk, d] into their cache slots."""
+    import torch
+    io = _paged_dtype(shape)
+    row, cache = shape.N * shape.Hk * shape.d, shape.n_pages * shape.Hk * shape.page_size * shape.d
+    args = _paged_args("moda_cache_append", (
+        ("k_new", k_new, row, io), ("v_new", v_new, row, io), ("slot_map", slot_map, shape.N, torch.int64),
+        ("k_cache", k_cache, cache, io), ("v_cache", v_cache, cache, io)))
+    _check(load().moda_cache_append(ctypes.byref(shape), *args, _stream(stream)), "moda_cache_append")
+
+
+def moda_tree_mask(shape: moda_paged_shape, parent, cu_new, held_len, mask, position, stream=None):
+    """Ancestor bits (int32 words) and positions of drafted trees; held_len
+    may be None (positions from 0)."""
+    import torch
+    i32, B, N = torch.int32, max(0, shape.B), shape.N
+    args = _paged_args("moda_tree_mask", (
+        ("parent", parent, N, i32), ("cu_new", cu_new, B + 1, i32), ("held_len", held_len, B, i32),
+        ("mask", mask, N * shape.mask_words, i32), ("position", position, N, i32)))
+    _check(load().moda_tree_mask(ctypes.byref(shape), *args, _stream(stream)), "moda_tree_mask")
+
+
+def moda_tree_decode_workspace_size(shape: moda_paged_shape) -> int:
+    n = load().moda_tree_decode_workspace_size(ctypes.byref(shape))
+    if n == ctypes.c_size_t(-1).value:   # report the validation error itself
+        _check(load().moda_tree_decode(ctypes.byref(shape), *([None] * 11), None, 0, None),
+               "moda_tree_decode_workspace_size")
+    return int(n)
+
+
+def moda_tree_decode(shape: moda_paged_shape, q, k_cache, v_cache, Kd, Vd, block_table, held_len, cu_new, mask,
+                     o, lse, ws, ws_bytes: int, stream=None):
+    """Attention of the new tokens (a tree by its mask rows, or chains with
+    mask None) over the paged cache and their own depth rows."""
+    import torch
+    io, i32 = _paged_dtype(shape), torch.int32
+    B, N, Hk, d = max(0, shape.B), shape.N, shape.Hk, shape.d
+    row, dep, cache = N * shape.Hq * d, N * Hk * shape.L * d, shape.n_pages * Hk * shape.page_size * d
+    args = _paged_args("moda_tree_decode", (
+        ("q", q, row, io), ("k_cache", k_cache, cache, io), ("v_cache", v_cache, cache, io), ("Kd", Kd, dep, io),
+        ("Vd", Vd, dep, io), ("block_table", block_table, B * shape.max_pages, i32),
+        ("held_len", held_len, B, i32), ("cu_new", cu_new, B + 1, i32), ("mask", mask, N * shape.mask_words, i32),
+        ("o", o, row, io), ("lse", lse, N * shape.Hq, torch.float32), ("ws", ws, int(ws_bytes), torch.uint8)))
+    _check(load().moda_tree_decode(ctypes.byref(shape), *args, int(ws_bytes), _stream(stream)),
+           "moda_tree_decode")
 
 
 def moda_selftest_wait_timeout(stream=None):

@@ -307,6 +307,9 @@ moda_status moda_check_status(moda_stream_t stream) {
         e = cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
         if (e != cudaSuccess) return cuda_fail(e, "status clear");
         if (v & kStatusTimeout) return fail(MODA_ERR_TIMEOUT, "a kernel wait timed out");
+        if (v & kStatusBadIndex)
+            return fail(MODA_ERR_INVALID_ARG,
+                        "a paged call met a length, page, slot or parent on the device that was out of range");
     }
     return MODA_OK;
 }
@@ -335,6 +338,6 @@ moda_status moda_set_phase_events(void* const* events, int n) {
     return MODA_OK;
 }
 
-int moda_version(void) { return 10200; }
+int moda_version(void) { return 10300; }
 
 }  // extern "C"

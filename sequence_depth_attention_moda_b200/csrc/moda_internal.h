@@ -21,9 +21,20 @@ struct Problem {
     int depth_layer;    // 1: Kd, Vd (and dKd, dVd) layer-major [L, B, Hk, T, d]
 };
 
+// A validated paged problem (moda_paged_shape); the fields a call does not use
+// stay 0.
+struct Paged {
+    int B, N, Hq, Hk, G, d, L;
+    int page, page_shift, n_pages, max_pages, words;
+    int elem_bytes;     // 2 (bf16) or 4 (fp32)
+    int win_lo, Lw;     // first depth row in the window, rows in it
+    float scale_log2;
+};
+
 // Kernel-side status bits written into the per-device status word.
 enum : unsigned int {
     kStatusTimeout = 1u,   // a bounded mbarrier / flag wait ran out
+    kStatusBadIndex = 2u,  // a length, page, slot or parent on the device was out of range
 };
 
 // Address of the calling device's status word (device memory), or nullptr.

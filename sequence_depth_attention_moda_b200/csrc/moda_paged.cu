@@ -1,0 +1,604 @@
+// moda_paged.cu -- the paged KV cache behind the attention of drafted tokens:
+// pages and slots from request lengths (moda_page_plan), new keys and values
+// into their slots (moda_cache_append), ancestor bits of drafted trees
+// (moda_tree_mask), and the C entry points of these and of moda_tree_decode.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+#include <initializer_list>
+#include <utility>
+
+#include "moda.h"
+#include "moda_internal.h"
+#include "moda_tree.cuh"
+
+namespace moda {
+namespace {
+
+// ------------------------------------------------------------------ plan ----
+// Page lists from lengths.  Request b holds have_b = ceil(held/P) pages and is
+// to hold need_b = ceil(want/P).  With exclusive prefixes over the requests,
+// drop_b of the pages given back (have - need where positive) and take_b of
+// those asked for, and top = count + sum of drops, released page r of the call
+// goes to place top-1-r of the free list and asked-for page q comes from place
+// top-1-q: a stack, the first request's pages on top, so that giving back what
+// a call took restores the list.  A request is served whole or not at all: if it
+// needs no page, or take_b + its own pages <= top.
+//
+// Bound by latency, not by bytes: one launch of one cluster of 8 CTAs.  Every
+// CTA adds up all requests (8 KB for 1024 of them); the page moves and the
+// slots are dealt over the cluster's 128 warps, and the two hand-overs (released
+// pages written before any is taken, table entries written before slots read
+// them) are cluster barriers.
+constexpr int kPlanCtas = 8;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kSlotChunk = 128;      // tokens a warp takes at a time
+constexpr int kMaxPlanRequests = 16384;
+
+struct PlanArgs {
+    const int *held, *want;
+    int *table, *free_pages, *free_count, *cu, *granted;
+    long long* slots;
+    unsigned int* status;
+    int B, N, page_shift, n_pages, max_pages;
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Exclusive prefix of `mine` over the CTA's threads; *total gets the sum.
+__device__ __forceinline__ long long block_prefix(long long mine, long long* warp_sum, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    long long base = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) {
+        if (w < warp) base += warp_sum[w];
+        sum += warp_sum[w];
+    }
+    *total = sum;
+    return base + inc - mine;
+}
+
+struct PlanRequest {
+    int held, want, have, need;      // clamped; need = have where the request cannot fit its row
+    bool fits;
+};
+__device__ __forceinline__ PlanRequest plan_request(const PlanArgs& a, int b) {
+    PlanRequest r;
+    const int P1 = (1 << a.page_shift) - 1;
+    const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+    const int h = __ldg(a.held + b), w = __ldg(a.want + b);
+    r.held = static_cast<int>(min(static_cast<long long>(max(h, 0)), cap));
+    r.want = max(w, 0);
+    if (r.held != h || r.want != w) atomicOr(a.status, kStatusBadIndex);
+    r.fits = r.want <= cap;
+    r.have = static_cast<int>((static_cast<long long>(r.held) + P1) >> a.page_shift);
+    r.need = r.fits ? static_cast<int>((static_cast<long long>(r.want) + P1) >> a.page_shift) : r.have;
+    return r;
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+page_plan_kernel(const __grid_constant__ PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    __shared__ long long warp_sum[kPlanWarps];
+    int* s_cu = plan_smem;               // [B+1]
+    int* s_take = s_cu + a.B + 1;        // [B], -1: refused
+    int* s_drop = s_take + a.B;          // [B]
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int gwarp = static_cast<int>(cluster_rank()) * kPlanWarps + (tid >> 5);
+    const int n_warps = kPlanCtas * kPlanWarps;
+    const int ch = (a.B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
+
+    // pages asked for (high half) and given back (low half)
+    long long mine = 0, total;
+    for (int b = b0; b < b1; ++b) {
+        const PlanRequest r = plan_request(a, b);
+        mine += (static_cast<long long>(max(r.need - r.have, 0)) << 32) + max(r.have - r.need, 0);
+    }
+    long long at = block_prefix(mine, warp_sum, &total);
+    const int count0 = __ldcg(a.free_count);
+    const int count = min(max(count0, 0), a.n_pages);
+    const long long top = count + (total & 0xffffffffll);
+    if (count != count0 || top > a.n_pages) atomicOr(a.status, kStatusBadIndex);
+    // what is served: its tokens and pages
+    long long tokens = 0, pages = 0;
+    for (int b = b0; b < b1; ++b) {
+        const PlanRequest r = plan_request(a, b);
+        const int take = max(r.need - r.have, 0), drop = max(r.have - r.need, 0);
+        const int take0 = static_cast<int>(at >> 32), drop0 = static_cast<int>(at & 0xffffffffll);
+        at += (static_cast<long long>(take) << 32) + drop;
+        const bool served = r.fits && (take == 0 || static_cast<long long>(take0) + take <= top);
+        s_take[b] = served ? take0 : -1;
+        s_drop[b] = drop0;
+        if (served) {
+            tokens += max(r.want - r.held, 0);
+            pages += take;
+        }
+    }
+    long long n_pages_granted, n_tokens;
+    block_prefix(pages, warp_sum, &n_pages_granted);
+    long long c = block_prefix(tokens, warp_sum, &n_tokens);
+    for (int b = b0; b < b1; ++b) {
+        const PlanRequest r = plan_request(a, b);
+        s_cu[b] = static_cast<int>(min(c, 0x7fffffffll));
+        const bool served = s_take[b] >= 0;
+        if (cluster_rank() == 0) {
+            a.cu[b] = s_cu[b];
+            a.granted[b] = served ? r.want : r.held;
+        }
+        if (served) c += max(r.want - r.held, 0);
+    }
+    if (tid == 0) {
+        s_cu[a.B] = static_cast<int>(min(n_tokens, 0x7fffffffll));
+        if (cluster_rank() == 0) {
+            a.cu[a.B] = s_cu[a.B];
+            if (n_tokens > a.N) atomicOr(a.status, kStatusBadIndex);
+        }
+    }
+    __syncthreads();
+
+    // released pages onto the list
+    for (int b = gwarp; b < a.B; b += n_warps) {
+        const PlanRequest r = plan_request(a, b);
+        int* row = a.table + static_cast<size_t>(b) * a.max_pages;
+        for (int k = r.need + lane; k < r.have; k += 32) {
+            const long long place = top - 1 - (s_drop[b] + k - r.need);
+            const int page = __ldcg(row + k);
+            if (place < a.n_pages) a.free_pages[place] = page;
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) atomicOr(a.status, kStatusBadIndex);
+            row[k] = -1;
+        }
+    }
+    cluster_barrier();
+    // asked-for pages off it
+    for (int b = gwarp; b < a.B; b += n_warps) {
+        if (s_take[b] < 0) continue;
+        const PlanRequest r = plan_request(a, b);
+        int* row = a.table + static_cast<size_t>(b) * a.max_pages;
+        for (int k = r.have + lane; k < r.need; k += 32) {
+            const long long place = top - 1 - (s_take[b] + k - r.have);
+            row[k] = place < a.n_pages ? __ldcg(a.free_pages + place) : -1;
+        }
+    }
+    if (cluster_rank() == 0 && tid == 0)
+        *a.free_count = static_cast<int>(min(top - n_pages_granted, static_cast<long long>(a.n_pages)));
+    cluster_barrier();
+    // a slot a token
+    const int n_in = min(s_cu[a.B], a.N);
+    const long long chunks = (static_cast<long long>(a.N) + kSlotChunk - 1) / kSlotChunk;
+    for (long long ck = gwarp; ck < chunks; ck += n_warps) {
+        const long long t0 = ck * kSlotChunk;
+        int lo = 0, hi = a.B - 1;            // the last request that starts at or before t0
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_cu[mid] <= t0) lo = mid;
+            else hi = mid - 1;
+        }
+        int b = lo;
+#pragma unroll
+        for (int u = 0; u < kSlotChunk / 32; ++u) {
+            const long long t = t0 + 32 * u + lane;
+            if (t >= a.N) break;
+            long long slot = -1;
+            if (t < n_in) {
+                while (s_cu[b + 1] <= t) ++b;
+                const int key = plan_request(a, b).held + static_cast<int>(t - s_cu[b]);
+                const int page = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
+                if (page >= 0) slot = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            }
+            a.slots[t] = slot;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- append ----
+// A copy of N rows of Hk*d elements for K and for V, 16 bytes a thread and
+// access; a head's d elements are contiguous on both sides (128 to 512 bytes).
+// Bound by HBM: every byte is read once and written once.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;
+
+struct AppendArgs {
+    const uint4 *k, *v;
+    uint4 *kc, *vc;
+    const long long* slots;
+    unsigned int* status;
+    long long n_slots, n_chunks;     // cache slots; N * row_chunks
+    int Hk, head_chunks, row_chunks, page_shift;
+};
+
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+    const long long first = static_cast<long long>(blockIdx.x) * (kAppendThreads * kAppendUnroll);
+    const long long tok0 = first / a.row_chunks;
+    const unsigned c0 = static_cast<unsigned>(first - tok0 * a.row_chunks);
+    uint4 kv[kAppendUnroll], vv[kAppendUnroll];
+    long long dst[kAppendUnroll];
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u) {
+        const unsigned i = c0 + u * kAppendThreads + threadIdx.x;
+        const unsigned dt = i / static_cast<unsigned>(a.row_chunks);
+        const unsigned c = i - dt * a.row_chunks;
+        const long long tok = tok0 + dt;
+        const long long src = tok * a.row_chunks + c;
+        dst[u] = -1;
+        if (src >= a.n_chunks) continue;
+        const long long slot = __ldg(a.slots + tok);
+        if (slot >= 0 && slot < a.n_slots) {
+            const unsigned hk = c / static_cast<unsigned>(a.head_chunks);
+            const long long page = slot >> a.page_shift;
+            const long long off = slot & ((1ll << a.page_shift) - 1);
+            dst[u] = (((page * a.Hk + hk) << a.page_shift) + off) * a.head_chunks + (c - hk * a.head_chunks);
+            kv[u] = __ldcs(a.k + src);
+            vv[u] = __ldcs(a.v + src);
+        } else if (slot != -1) {
+            atomicOr(a.status, kStatusBadIndex);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u)
+        if (dst[u] >= 0) {
+            a.kc[dst[u]] = kv[u];
+            a.vc[dst[u]] = vv[u];
+        }
+}
+
+// ------------------------------------------------------------------ mask ----
+// mask[i] = bit i | mask[parent[i]]: each thread walks one token's ancestors
+// (parents are earlier tokens, so the walk ends) through the parents in shared
+// memory and collects four words at a time.  Random trees are shallow; a chain
+// of n costs n steps of about 30 cycles, which is still less than the launch
+// for the n of a draft.
+constexpr int kMaskThreads = 128;
+constexpr int kMaskGroup = 4;        // words a walk collects
+constexpr int kMaxMaskWords = 64;
+
+struct MaskArgs {
+    const int *parent, *cu, *held;   // held: NULL counts positions from 0
+    uint32_t* mask;
+    int* position;
+    unsigned int* status;
+    int B, N, words;
+};
+
+__global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const __grid_constant__ MaskArgs a) {
+    __shared__ int up[32 * kMaxMaskWords];
+    const int b = blockIdx.x;
+    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+    const int h = a.held ? __ldg(a.held + b) : 0;
+    const int first = min(max(c0, 0), a.N);
+    const int n = static_cast<int>(max(0ll, min(static_cast<long long>(c1) - c0,
+                                                min(static_cast<long long>(a.N - first), 32ll * a.words))));
+    bool bad = first != c0 || n != c1 - c0;
+    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+        int p = __ldg(a.parent + first + i);
+        if (p < -1 || p >= i) {          // no earlier token: taken as the root's child
+            bad = true;
+            p = -1;
+        }
+        up[i] = p;
+    }
+    if (bad) atomicOr(a.status, kStatusBadIndex);
+    __syncthreads();
+    const int groups = (a.words + kMaskGroup - 1) / kMaskGroup;
+    for (int x = threadIdx.x; x < n * groups; x += kMaskThreads) {
+        const int i = x / groups, w0 = (x - i * groups) * kMaskGroup;
+        uint32_t w[kMaskGroup] = {};
+        int depth = -1;
+        for (int t = i; t >= 0; t = up[t]) {
+            const int at = (t >> 5) - w0;
+            const uint32_t bit = 1u << (t & 31);
+#pragma unroll
+            for (int k = 0; k < kMaskGroup; ++k) w[k] |= at == k ? bit : 0u;
+            ++depth;
+        }
+        uint32_t* row = a.mask + static_cast<size_t>(first + i) * a.words + w0;
+#pragma unroll
+        for (int k = 0; k < kMaskGroup; ++k)
+            if (w0 + k < a.words) row[k] = w[k];
+        if (w0 == 0) a.position[first + i] = h + depth;
+    }
+}
+
+// ------------------------------------------------------------------- host ---
+bool power_of_two(int x) { return x > 0 && (x & (x - 1)) == 0; }
+
+moda_status failf(moda_status s, const char* fmt, long long x = 0, long long y = 0, long long z = 0) {
+    char msg[240];
+    snprintf(msg, sizeof(msg), fmt, x, y, z);
+    return api_fail(s, msg);
+}
+
+// What every paged call checks: sizes of the batch and of the pages.
+moda_status check_pages(const moda_paged_shape* s, Paged* p) {
+    if (!s) return failf(MODA_ERR_INVALID_ARG, "shape is NULL");
+    if (s->B < 0 || s->N < 0) return failf(MODA_ERR_INVALID_ARG, "B=%lld N=%lld must be >= 0", s->B, s->N);
+    if (!power_of_two(s->page_size) || s->page_size < 8 || s->page_size > 1024)
+        return failf(MODA_ERR_INVALID_ARG, "page_size=%lld must be a power of two in 8..1024", s->page_size);
+    if (s->n_pages < 1 || s->max_pages < 1)
+        return failf(MODA_ERR_INVALID_ARG, "n_pages=%lld and max_pages=%lld must be >= 1", s->n_pages, s->max_pages);
+    // positions and table entries are indexed with 32 bits
+    if (static_cast<double>(s->max_pages) * s->page_size > 2147483647.0 ||
+        static_cast<double>(s->B) * s->max_pages > 2147483647.0)
+        return failf(MODA_ERR_UNSUPPORTED, "max_pages=%lld too large for B=%lld requests of pages of %lld tokens",
+                     s->max_pages, s->B, s->page_size);
+    p->B = s->B; p->N = s->N; p->page = s->page_size; p->n_pages = s->n_pages; p->max_pages = s->max_pages;
+    p->page_shift = 0;
+    while ((1 << p->page_shift) < s->page_size) ++p->page_shift;
+    return MODA_OK;
+}
+
+moda_status check_words(const moda_paged_shape* s, Paged* p, bool needed) {
+    if (s->mask_words < (needed ? 1 : 0) || s->mask_words > kMaxMaskWords)
+        return failf(MODA_ERR_INVALID_ARG, "mask_words=%lld must be in %lld..%lld", s->mask_words, needed ? 1 : 0,
+                     kMaxMaskWords);
+    p->words = s->mask_words;
+    return MODA_OK;
+}
+
+// The cache's element type, heads and head dimension.
+moda_status check_cache(const moda_paged_shape* s, Paged* p) {
+    if (s->dtype != MODA_BF16 && s->dtype != MODA_FP32)
+        return failf(MODA_ERR_INVALID_ARG, "unknown dtype %lld", s->dtype);
+    if (s->Hk < 1) return failf(MODA_ERR_INVALID_ARG, "need Hk >= 1 (Hk=%lld)", s->Hk);
+    if (s->d != 64 && s->d != 128) return failf(MODA_ERR_UNSUPPORTED, "the paged calls support d in {64, 128} (d=%lld)", s->d);
+    if (static_cast<double>(s->n_pages) * s->Hk > 2147483647.0)
+        return failf(MODA_ERR_UNSUPPORTED, "n_pages=%lld of Hk=%lld heads pass 32-bit page indices", s->n_pages, s->Hk);
+    p->Hk = s->Hk; p->d = s->d;
+    p->elem_bytes = s->dtype == MODA_BF16 ? 2 : 4;
+    return MODA_OK;
+}
+
+moda_status check_tree(const moda_paged_shape* s, Paged* p) {
+    moda_status st;
+    if ((st = check_pages(s, p)) != MODA_OK || (st = check_words(s, p, false)) != MODA_OK ||
+        (st = check_cache(s, p)) != MODA_OK)
+        return st;
+    if (s->Hq < 1 || s->Hq % s->Hk != 0)
+        return failf(MODA_ERR_INVALID_ARG, "need Hq >= 1 and Hq %% Hk == 0 (Hq=%lld Hk=%lld)", s->Hq, s->Hk);
+    if (s->Hq / s->Hk > 64)
+        return failf(MODA_ERR_UNSUPPORTED, "moda_tree_decode supports G <= 64 (G=%lld)", s->Hq / s->Hk);
+    if (s->L < 0) return failf(MODA_ERR_INVALID_ARG, "L=%lld must be >= 0", s->L);
+    if (s->depth_window < 0 || s->depth_window > s->L)
+        return failf(MODA_ERR_INVALID_ARG, "depth_window=%lld must be in 0..L (L=%lld)", s->depth_window, s->L);
+    if (!(s->softmax_scale >= 0.0f) || std::isinf(s->softmax_scale))
+        return failf(MODA_ERR_INVALID_ARG, "softmax_scale must be finite (<= 0 for 1/sqrt(d))");
+    if (static_cast<double>(s->N) * s->Hq > 2147483647.0 || static_cast<double>(s->N) * s->Hk > 2147483647.0)
+        return failf(MODA_ERR_UNSUPPORTED, "N=%lld tokens of Hq=%lld heads pass 32-bit row indices", s->N, s->Hq);
+    p->Hq = s->Hq; p->G = s->Hq / s->Hk; p->L = s->L;
+    p->win_lo = s->depth_window > 0 ? s->L - s->depth_window : 0;
+    p->Lw = p->L - p->win_lo;
+    p->scale_log2 = (s->softmax_scale > 0.0f ? s->softmax_scale : 1.0f / std::sqrt(float(s->d))) * 1.4426950408889634f;
+    return MODA_OK;
+}
+
+moda_status check_ptrs(std::initializer_list<std::pair<const void*, const char*>> ptrs) {
+    char msg[120];
+    for (const auto& pr : ptrs) {
+        if (!pr.first) {
+            snprintf(msg, sizeof(msg), "%s is NULL", pr.second);
+            return api_fail(MODA_ERR_INVALID_ARG, msg);
+        }
+        if ((reinterpret_cast<uintptr_t>(pr.first) & 15u) != 0) {
+            snprintf(msg, sizeof(msg), "%s is not 16-byte aligned", pr.second);
+            return api_fail(MODA_ERR_MISALIGNED, msg);
+        }
+    }
+    return MODA_OK;
+}
+
+moda_status launched(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return MODA_OK;
+    char msg[200];
+    snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
+    return api_fail(MODA_ERR_CUDA, msg);
+}
+
+moda_status no_device() { return api_fail(MODA_ERR_CUDA, "no usable CUDA device"); }
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Nothing may be thrown across the C ABI (a full host heap, a broken mutex).
+template <typename F>
+moda_status guarded(F&& f) noexcept {
+    try {
+        return f();
+    } catch (...) {
+        return MODA_ERR_CUDA;
+    }
+}
+
+}  // namespace
+
+TreePlan tree_plan(const Paged& p) {
+    TreePlan t;
+    const int per = p.B > 0 ? (p.N + p.B - 1) / p.B : p.N;     // tokens of a request, on average
+    t.KT = 64;
+    t.rows = p.G <= 16 && static_cast<long long>(per) * p.G <= 16 ? 16 : 64;
+    t.sub = 1;
+    t.Tq = t.rows / p.G;
+    t.Tg = t.Tq * t.sub;
+    t.Lp = p.Lw > 0 ? p.Lw : 1;
+    t.dtok = t.Lp <= t.KT ? t.KT / t.Lp : 1;
+    t.dsplit = (t.Lp + t.KT - 1) / t.KT;
+    const long long rows = static_cast<long long>(p.N) * p.G;
+    t.rec_rows = rows < static_cast<long long>(t.Tg) * p.G ? static_cast<int>(rows) : t.Tg * p.G;
+    t.n_cta = device_sm_count() * (t.rows == 64 && p.d == 128 ? 1 : 2);
+    t.off_ml = round256(sizeof(tree::CtaHeader) * t.n_cta);
+    t.off_po = t.off_ml + round256(sizeof(float2) * 2 * t.n_cta * t.rec_rows);
+    t.bytes = t.off_po + round256(sizeof(float) * 2 * t.n_cta * t.rec_rows * p.d);
+    return t;
+}
+
+}  // namespace moda
+
+using namespace moda;
+
+extern "C" {
+
+moda_status moda_page_plan(const moda_paged_shape* shape, const int* held_len, const int* want_len,
+                           int* block_table, int* free_pages, int* free_count, int* cu_new,
+                           int* granted_len, long long* slot_map, moda_stream_t stream) {
+    return guarded([&]() -> moda_status {
+        Paged p{};
+        moda_status st = check_pages(shape, &p);
+        if (st != MODA_OK) return st;
+        if (p.B > kMaxPlanRequests)
+            return failf(MODA_ERR_UNSUPPORTED, "moda_page_plan supports B <= %lld (B=%lld)", kMaxPlanRequests, p.B);
+        if ((st = check_ptrs({{free_pages, "free_pages"}, {free_count, "free_count"}, {cu_new, "cu_new"}})) != MODA_OK)
+            return st;
+        if (p.B > 0 && (st = check_ptrs({{held_len, "held_len"}, {want_len, "want_len"}, {block_table, "block_table"},
+                                         {granted_len, "granted_len"}})) != MODA_OK)
+            return st;
+        if (p.N > 0 && (st = check_ptrs({{slot_map, "slot_map"}})) != MODA_OK) return st;
+        if (p.B > 0 && (granted_len == held_len || granted_len == want_len))
+            return failf(MODA_ERR_INVALID_ARG, "granted_len must not alias held_len or want_len");
+        PlanArgs a;
+        a.held = held_len; a.want = want_len; a.table = block_table; a.free_pages = free_pages;
+        a.free_count = free_count; a.cu = cu_new; a.granted = granted_len; a.slots = slot_map;
+        a.status = device_status_word();
+        if (!a.status) return no_device();
+        a.B = p.B; a.N = p.N; a.page_shift = p.page_shift; a.n_pages = p.n_pages; a.max_pages = p.max_pages;
+        const int smem = (3 * p.B + 1) * static_cast<int>(sizeof(int));
+        cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(page_plan_kernel),
+                                             (3 * kMaxPlanRequests + 1) * static_cast<int>(sizeof(int)));
+        if (e == cudaSuccess) {
+            page_plan_kernel<<<kPlanCtas, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+            e = cudaGetLastError();
+        }
+        return launched(e, "page plan launch");
+    });
+}
+
+moda_status moda_cache_append(const moda_paged_shape* shape, const void* k_new, const void* v_new,
+                              const long long* slot_map, void* k_cache, void* v_cache,
+                              moda_stream_t stream) {
+    return guarded([&]() -> moda_status {
+        Paged p{};
+        moda_status st;
+        if ((st = check_pages(shape, &p)) != MODA_OK || (st = check_cache(shape, &p)) != MODA_OK) return st;
+        if (p.N == 0) return MODA_OK;
+        if ((st = check_ptrs({{k_new, "k_new"}, {v_new, "v_new"}, {slot_map, "slot_map"}, {k_cache, "k_cache"},
+                              {v_cache, "v_cache"}})) != MODA_OK)
+            return st;
+        AppendArgs a;
+        a.k = static_cast<const uint4*>(k_new); a.v = static_cast<const uint4*>(v_new);
+        a.kc = static_cast<uint4*>(k_cache); a.vc = static_cast<uint4*>(v_cache);
+        a.slots = slot_map;
+        a.status = device_status_word();
+        if (!a.status) return no_device();
+        const long long row_chunks = static_cast<long long>(p.Hk) * (p.d * p.elem_bytes / 16);
+        if (row_chunks > (1 << 24)) return failf(MODA_ERR_UNSUPPORTED, "Hk=%lld too large", p.Hk);
+        a.Hk = p.Hk;
+        a.head_chunks = p.d * p.elem_bytes / 16;
+        a.row_chunks = static_cast<int>(row_chunks);
+        a.page_shift = p.page_shift;
+        a.n_slots = static_cast<long long>(p.n_pages) << p.page_shift;
+        a.n_chunks = row_chunks * p.N;
+        const long long per = kAppendThreads * kAppendUnroll;
+        const long long grid = (a.n_chunks + per - 1) / per;
+        if (grid > 0x7fffffffll) return failf(MODA_ERR_UNSUPPORTED, "N=%lld tokens are too many for one call", p.N);
+        cache_append_kernel<<<static_cast<unsigned>(grid), kAppendThreads, 0,
+                              reinterpret_cast<cudaStream_t>(stream)>>>(a);
+        return launched(cudaGetLastError(), "cache append launch");
+    });
+}
+
+moda_status moda_tree_mask(const moda_paged_shape* shape, const int* parent, const int* cu_new,
+                           const int* held_len, unsigned int* mask, int* position,
+                           moda_stream_t stream) {
+    return guarded([&]() -> moda_status {
+        Paged p{};
+        moda_status st;
+        if ((st = check_pages(shape, &p)) != MODA_OK || (st = check_words(shape, &p, true)) != MODA_OK) return st;
+        if (p.B == 0 || p.N == 0) return MODA_OK;
+        if ((st = check_ptrs({{parent, "parent"}, {cu_new, "cu_new"}, {mask, "mask"}, {position, "position"}})) != MODA_OK)
+            return st;
+        if (held_len && (st = check_ptrs({{held_len, "held_len"}})) != MODA_OK) return st;
+        MaskArgs a;
+        a.parent = parent; a.cu = cu_new; a.held = held_len; a.mask = mask; a.position = position;
+        a.status = device_status_word();
+        if (!a.status) return no_device();
+        a.B = p.B; a.N = p.N; a.words = p.words;
+        tree_mask_kernel<<<p.B, kMaskThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+        return launched(cudaGetLastError(), "tree mask launch");
+    });
+}
+
+size_t moda_tree_decode_workspace_size(const moda_paged_shape* shape) {
+    size_t bytes = static_cast<size_t>(-1);
+    guarded([&]() -> moda_status {
+        Paged p{};
+        const moda_status st = check_tree(shape, &p);
+        if (st == MODA_OK) bytes = p.B == 0 || p.N == 0 ? 0 : tree_plan(p).bytes;
+        return st;
+    });
+    return bytes;
+}
+
+moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const void* k_cache,
+                             const void* v_cache, const void* Kd, const void* Vd,
+                             const int* block_table, const int* held_len, const int* cu_new,
+                             const unsigned int* mask, void* o, float* lse, void* ws,
+                             size_t ws_bytes, moda_stream_t stream) {
+    return guarded([&]() -> moda_status {
+        Paged p{};
+        moda_status st = check_tree(shape, &p);
+        if (st != MODA_OK) return st;
+        if (p.B == 0 || p.N == 0) return MODA_OK;
+        if ((st = check_ptrs({{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}, {block_table, "block_table"},
+                              {held_len, "held_len"}, {cu_new, "cu_new"}, {o, "o"}, {lse, "lse"}, {ws, "ws"}})) != MODA_OK)
+            return st;
+        if (p.L > 0 && (st = check_ptrs({{Kd, "Kd"}, {Vd, "Vd"}})) != MODA_OK) return st;
+        if ((mask != nullptr) != (p.words > 0))
+            return failf(MODA_ERR_INVALID_ARG, "a mask needs mask_words >= 1, and mask_words = 0 (a chain) no mask "
+                         "(mask_words=%lld)", p.words);
+        if (mask && (st = check_ptrs({{mask, "mask"}})) != MODA_OK) return st;
+        unsigned int* status = device_status_word();
+        if (!status) return no_device();
+        const TreePlan t = tree_plan(p);
+        if (ws_bytes < t.bytes)
+            return failf(MODA_ERR_WORKSPACE, "moda_tree_decode needs %lld bytes of workspace (got %lld)",
+                         static_cast<long long>(t.bytes), static_cast<long long>(ws_bytes));
+        tree::TreeArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.q = q; a.kc = k_cache; a.vc = v_cache; a.kd = Kd; a.vd = Vd;
+        a.table = block_table; a.held = held_len; a.cu = cu_new; a.mask = mask;
+        a.o = o; a.lse = lse;
+        unsigned char* base = static_cast<unsigned char*>(ws);
+        a.hdr = reinterpret_cast<tree::CtaHeader*>(base);
+        a.ml = reinterpret_cast<float2*>(base + t.off_ml);
+        a.po = reinterpret_cast<float*>(base + t.off_po);
+        a.status = status;
+        a.B = p.B; a.N = p.N; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.G; a.L = p.L; a.Lw = p.Lw; a.win_lo = p.win_lo;
+        a.page_shift = p.page_shift; a.n_pages = p.n_pages; a.max_pages = p.max_pages; a.words = p.words;
+        a.Tq = t.Tq; a.Tg = t.Tg; a.KT = t.KT; a.Lp = t.Lp; a.dtok = t.dtok; a.dsplit = t.dsplit;
+        a.rec_rows = t.rec_rows; a.n_cta = t.n_cta; a.scale_log2 = p.scale_log2;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        phase_mark(0, s);
+        cudaError_t e = launch_tree_simt(p, t, a, s);
+        if (e == cudaSuccess) e = launch_tree_combine(p, t, a, s);
+        if (e == cudaSuccess) phase_mark(1, s);
+        return launched(e, "tree decode launch");
+    });
+}
+
+}  // extern "C"

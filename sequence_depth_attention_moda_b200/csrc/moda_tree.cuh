@@ -1,0 +1,351 @@
+// moda_tree.cuh -- what the two paths of the attention of drafted tokens over
+// a paged cache share: the arguments, the schedule, the visible sets and the
+// partial records (moda_tree_simt.cu: CUDA cores, fp32; moda_tree_sm100.cu:
+// tensor cores, bf16; moda_tree_combine.cu: merging split jobs).
+//
+// Work.  A job is (request b, KV head hk, group of Tg consecutive new tokens);
+// its rows are the G query heads of each token, row = token * G + head.  A job
+// reads tiles of KT key rows: first its sequence tiles (keys 0 .. held+n-1 of
+// the request, through the block table), then the depth tiles of its tokens.
+// Only the keys from `held` on and the depth rows are masked.  The jobs' tiles
+// form one list, in the order request, KV head, group, tile; CTA c of P owns
+// the contiguous range [c*X/P, (c+1)*X/P) of its X tiles.  Lengths live on the
+// device (a captured graph replays with other ones), so every CTA adds up the
+// list itself.  A job that one CTA owns whole is written out by it; of a job
+// cut at a range's end every CTA leaves one (m, l, o) record a row, and the
+// combine kernel merges them in CTA order.  At most two of a CTA's jobs can be
+// cut (its first and its last), so the records take 2 slots a CTA whatever
+// the lengths.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "moda_internal.h"
+#include "moda_ptx.cuh"
+
+namespace moda {
+namespace tree {
+
+// The job that holds a CTA's first tile, left for the combine kernel.
+struct CtaHeader {
+    long long x_total;     // tiles of the whole call
+    long long job_start;   // first tile of the job
+    int nt;                // its tiles
+    int b, hk, group;
+};
+
+struct TreeArgs {
+    const void *q, *kc, *vc, *kd, *vd;   // [N,Hq,D], cache [n_pages,Hk,page,D], [N,Hk,L,D]
+    const int *table, *held, *cu;        // [B,max_pages], [B], [B+1]
+    const uint32_t* mask;                // [N,words] or NULL (chain)
+    void* o;                             // [N,Hq,D]
+    float* lse;                          // [N,Hq]
+    CtaHeader* hdr;                      // [n_cta]
+    float2* ml;                          // [2*n_cta][rec_rows]: m (base 2), l (negative: see row_poisoned)
+    float* po;                           // [2*n_cta][rec_rows][D]
+    unsigned int* status;
+    int B, N, Hq, Hk, G, L, Lw, win_lo;  // Lw: depth rows in the window
+    int page_shift, n_pages, max_pages, words;
+    int Tq, Tg;                          // tokens per row tile, per job (Tg = Tq or 2*Tq)
+    int KT;                              // key rows per tile
+    int Lp, dtok, dsplit;                // depth tiles: rows a token takes, tokens per tile (Lw <= KT),
+                                         // tiles per token (Lw > KT)
+    int rec_rows, n_cta;
+    float scale_log2;
+};
+
+// A request's clamped lengths.  What lies outside the tables' bounds is cut
+// off, so that no index below leaves its array, and reported.
+struct Request {
+    int held, n, cu0;
+};
+__device__ __forceinline__ Request load_request(const TreeArgs& a, int b) {
+    Request r;
+    const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+    const int h = __ldg(a.held + b), c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+    r.held = static_cast<int>(min(static_cast<long long>(max(h, 0)), cap));
+    r.cu0 = min(max(c0, 0), a.N);
+    long long n = static_cast<long long>(c1) - c0;
+    n = min(n, static_cast<long long>(a.N - r.cu0));
+    n = min(n, cap - r.held);
+    if (a.mask) n = min(n, 32ll * a.words);
+    r.n = static_cast<int>(max(n, 0ll));
+    if (r.held != h || r.cu0 != c0 || r.n != c1 - c0) atomicOr(a.status, kStatusBadIndex);
+    return r;
+}
+
+__device__ __forceinline__ int dep_tiles_of(const TreeArgs& a, int tokens) {
+    if (a.Lw == 0 || tokens <= 0) return 0;
+    return a.Lw <= a.KT ? (tokens + a.dtok - 1) / a.dtok : tokens * a.dsplit;
+}
+
+struct Job {
+    int b, hk, group;
+    Request r;
+    int tok0, ntok;      // the group's tokens, relative to the request's first
+    int nseq, ndep0, nt; // sequence tiles, depth tiles of the first Tq tokens, all tiles
+};
+
+__device__ __forceinline__ int groups_of(const TreeArgs& a, const Request& r) { return (r.n + a.Tg - 1) / a.Tg; }
+
+__device__ __forceinline__ void set_group(const TreeArgs& a, Job& j, int group) {
+    j.group = group;
+    j.tok0 = group * a.Tg;
+    j.ntok = min(a.Tg, j.r.n - j.tok0);
+    // a chain's group sees no key behind its last token
+    const int keys = j.r.held + (a.mask ? j.r.n : j.tok0 + j.ntok);
+    j.nseq = (keys + a.KT - 1) / a.KT;
+    j.ndep0 = dep_tiles_of(a, min(j.ntok, a.Tq));
+    j.nt = j.nseq + j.ndep0 + dep_tiles_of(a, j.ntok - a.Tq);
+}
+
+// Tiles of one KV head of a request.
+__device__ __forceinline__ long long head_tiles(const TreeArgs& a, const Request& r) {
+    Job j;
+    j.r = r;
+    const int ng = groups_of(a, r);
+    if (ng == 0) return 0;
+    if (a.mask) {                       // all groups but the last are alike
+        set_group(a, j, ng - 1);
+        long long t = j.nt;
+        if (ng > 1) {
+            set_group(a, j, 0);
+            t += static_cast<long long>(j.nt) * (ng - 1);
+        }
+        return t;
+    }
+    long long t = 0;
+    for (int g = 0; g < ng; ++g) {
+        set_group(a, j, g);
+        t += j.nt;
+    }
+    return t;
+}
+
+// Where a CTA starts, in shared memory; written by schedule().
+struct Start {
+    long long warp_sum[32];
+    long long x_total;
+    int b, hk, group, i0;    // first job and the first tile within it
+    int count;               // tiles of this CTA
+};
+
+__device__ __forceinline__ long long range_begin(long long c, long long x, long long p) { return c * x / p; }
+
+// Called by all threads of the CTA: finds the CTA's range and writes its
+// header.  Ends with a __syncthreads.
+__device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
+    const int nth = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
+    const int lane = tid & 31, warp = tid >> 5;
+    const int ch = (a.B + nth - 1) / nth;
+    const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += head_tiles(a, load_request(a, b)) * a.Hk;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) s->warp_sum[warp] = inc;
+    if (tid == 0) s->count = 0;
+    __syncthreads();
+    long long base = 0, total = 0;
+    for (int w = 0; w < (nth >> 5); ++w) {
+        if (w < warp) base += s->warp_sum[w];
+        total += s->warp_sum[w];
+    }
+    const long long pre = base + inc - mine;
+    const long long P = min(static_cast<long long>(a.n_cta), total);
+    const long long c = blockIdx.x;
+    CtaHeader h;
+    h.x_total = total;
+    h.job_start = 0;
+    h.nt = h.b = h.hk = h.group = 0;
+    if (c < P) {
+        const long long lo = range_begin(c, total, P), hi = range_begin(c + 1, total, P);
+        if (pre <= lo && lo < pre + mine) {
+            long long at = pre;
+            for (int b = b0; b < b1; ++b) {
+                Job j;
+                j.r = load_request(a, b);
+                const long long ht = head_tiles(a, j.r);
+                if (lo >= at + ht * a.Hk) {
+                    at += ht * a.Hk;
+                    continue;
+                }
+                const int hk = static_cast<int>((lo - at) / ht);
+                at += ht * hk;
+                int g = 0;
+                for (;; ++g) {
+                    set_group(a, j, g);
+                    if (lo < at + j.nt) break;
+                    at += j.nt;
+                }
+                s->b = b;
+                s->hk = hk;
+                s->group = g;
+                s->i0 = static_cast<int>(lo - at);
+                s->count = static_cast<int>(hi - lo);
+                h.job_start = at;
+                h.nt = j.nt;
+                h.b = b;
+                h.hk = hk;
+                h.group = g;
+                a.hdr[c] = h;
+                break;
+            }
+        }
+    } else if (tid == 0) {
+        a.hdr[c] = h;
+    }
+    if (tid == 0) s->x_total = total;
+    __syncthreads();
+}
+
+// Walks a CTA's jobs.
+struct Walk {
+    Job j;
+    int i0, i1;      // this CTA's tiles of the job
+    int left;        // tiles left behind them
+    int seg;         // 0 for the first
+    __device__ __forceinline__ bool begin(const TreeArgs& a, const Start& s) {
+        seg = 0;
+        left = s.count;
+        if (left <= 0) return false;
+        j.b = s.b;
+        j.hk = s.hk;
+        j.r = load_request(a, s.b);
+        set_group(a, j, s.group);
+        take(s.i0);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const TreeArgs& a) {
+        if (left <= 0) return false;
+        int g = j.group + 1;
+        if (g * a.Tg >= j.r.n) {
+            g = 0;
+            if (++j.hk == a.Hk) {
+                j.hk = 0;
+                do {
+                    if (++j.b >= a.B) return false;
+                    j.r = load_request(a, j.b);
+                } while (j.r.n == 0);
+            }
+        }
+        set_group(a, j, g);
+        ++seg;
+        take(0);
+        return true;
+    }
+    // Whether this CTA owns the job whole (then it writes the outputs itself).
+    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == j.nt; }
+    __device__ __forceinline__ int slot(const TreeArgs&) const {
+        return 2 * static_cast<int>(blockIdx.x) + (seg ? 1 : 0);
+    }
+
+   private:
+    __device__ __forceinline__ void take(int first) {
+        i0 = first;
+        i1 = min(j.nt, first + left);
+        left -= i1 - i0;
+    }
+};
+
+// ------------------------------------------------------------ visible sets --
+// Bit c set for lo <= c < hi, 0 <= c < 32.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 32);
+    if (lo >= hi) return 0u;
+    return (0xffffffffu >> (32 - (hi - lo))) << lo;
+}
+
+// Which of the 32 sequence keys from key `k0` on the token sees: every held
+// key, and of the request's n new keys those whose bit its mask row has (in a
+// chain: those up to itself).
+__device__ __forceinline__ uint32_t seq_visible(const TreeArgs& a, const Request& r, int token, int k0) {
+    const int rel = k0 - r.held;
+    if (rel <= -32) return 0xffffffffu;
+    if (!a.mask) return bits_between(0, min(token + 1, r.n) - rel);
+    const uint32_t* row = a.mask + static_cast<size_t>(r.cu0 + token) * a.words;
+    const int w = rel >> 5;             // floor
+    auto word = [&](int x) -> uint32_t { return x < 0 ? 0xffffffffu : (x < a.words ? __ldg(row + x) : 0u); };
+    return __funnelshift_r(word(w), word(w + 1), rel & 31) & bits_between(0, r.n - rel);
+}
+
+// Which of 32 rows from row `c0` on of depth tile `dt` (of the row tile's
+// tokens) are the depth rows of the row tile's token `t`.
+__device__ __forceinline__ uint32_t dep_visible(const TreeArgs& a, int t, int dt, int c0) {
+    if (a.Lw <= a.KT) {
+        const int at = (t - dt * a.dtok) * a.Lp - c0;
+        return (t >= dt * a.dtok && t < (dt + 1) * a.dtok) ? bits_between(at, at + a.Lw) : 0u;
+    }
+    const int tok = dt / a.dsplit;
+    return tok == t ? bits_between(0, a.Lw - (dt - tok * a.dsplit) * a.KT - c0) : 0u;
+}
+
+// The page of a request that holds key `key`; -1 (and a status) for an entry
+// that names no page of the cache.
+__device__ __forceinline__ int page_of(const TreeArgs& a, int b, int key) {
+    const int p = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
+    if (static_cast<unsigned>(p) < static_cast<unsigned>(a.n_pages)) return p;
+    atomicOr(a.status, kStatusBadIndex);
+    return -1;
+}
+
+// ------------------------------------------------- values that are not finite --
+// P V sums over all rows of a tile, and 0 * Inf is NaN: an infinity or a NaN
+// in a value that only some of a tile's query rows see would reach the others.
+// So in the rows of V that are masked for anybody (new keys, depth rows) such
+// elements are replaced by 0 before the product and the record is marked; the
+// (rare) marked rows add them back here, each from the keys it sees.  Added
+// without its weight: p > 0 does not change an infinity or a NaN.
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename E, int D>
+__device__ __noinline__ float not_finite_sum(const TreeArgs& a, const Job& j, int token, int col) {
+    float sum = 0.0f;
+    auto add = [&](const E* p) {
+        const float v = to_float(*p);
+        if (!isfinite(v)) sum += v;
+    };
+    const int page = 1 << a.page_shift;
+    for (int k = 0; k < j.r.n; ++k) {
+        const int key = j.r.held + k;
+        if (!(seq_visible(a, j.r, token, key) & 1u)) continue;
+        const int p = page_of(a, j.b, key);
+        if (p < 0) continue;
+        add(static_cast<const E*>(a.vc) +
+            ((static_cast<size_t>(p) * a.Hk + j.hk) * page + (key & (page - 1))) * D + col);
+    }
+    const size_t row = (static_cast<size_t>(j.r.cu0 + token) * a.Hk + j.hk) * a.L;
+    for (int l = a.win_lo; l < a.L; ++l) add(static_cast<const E*>(a.vd) + (row + l) * D + col);
+    return sum;
+}
+
+// A record's l is a sum of exponentials, never negative: its sign carries the
+// mark.  (-0 for a marked row that saw no key.)
+__device__ __forceinline__ bool row_poisoned(float l) { return signbit(l); }
+
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;   // an empty row: log 0
+}
+
+}  // namespace tree
+
+// One path's plan for a shape: row tile and tile sizes, CTAs, workspace.
+struct TreePlan {
+    int rows, sub, KT;       // query rows per row tile, row tiles per job, keys per tile
+    int Tq, Tg, Lp, dtok, dsplit, rec_rows, n_cta;
+    size_t off_ml, off_po, bytes;
+};
+TreePlan tree_plan(const Paged& p);
+cudaError_t launch_tree_simt(const Paged& p, const TreePlan& t, tree::TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_combine(const Paged& p, const TreePlan& t, const tree::TreeArgs& a, cudaStream_t s);
+
+}  // namespace moda

@@ -1,0 +1,508 @@
+"""The paged calls on the GPU against the oracle: page plans, appends, tree
+masks, the attention of drafted tokens, and a run of them together."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sequence_depth_attention_moda_b200 as moda
+from moda_cases import Guarded
+from paged_cases import (Tree, check_tree, make_tree, mask_words, out_bound, random_parents, to_device, torch_dtype)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    yield
+    moda.moda_check_status()
+
+
+# ----------------------------------------------------------------------- plan --
+def dev_i32(v):
+    return torch.as_tensor(np.asarray(v, dtype=np.int32), device=DEV)
+
+
+def run_plan(P, N, held, want, table, free, count, n_pages):
+    """The call on guarded outputs; table and free are updated in place."""
+    B = len(held)
+    sh = moda.make_paged_shape(B, N, 1, 1, 128, 0, P, n_pages, table.shape[1])
+    gd = Guarded()
+    cu, granted = (gd.empty(n, (k,), torch.int32, DEV, output=False) for n, k in (("cu", B + 1), ("granted", B)))
+    slots = gd.empty("slots", (N,), torch.int64, DEV, output=False)
+    moda.moda_page_plan(sh, dev_i32(held), dev_i32(want), table, free, count, cu, granted, slots)
+    gd.check()
+    return cu.tolist(), granted.tolist(), slots.tolist()
+
+
+def table_of(rows, max_pages):
+    t = np.full((len(rows), max_pages), -1, dtype=np.int32)
+    for b, r in enumerate(rows):
+        t[b, : len(r)] = r
+    return dev_i32(t)
+
+
+def start_pages(rng, held, P, n_pages):
+    order = list(map(int, rng.permutation(n_pages)))
+    rows = []
+    for h in held:
+        k = -(-int(h) // P)
+        rows.append(order[:k])
+        order = order[k:]
+    return rows, order
+
+
+PLANS = [  # B, P, most held, most added, spare pages
+    (1, 8, 0, 1, 1), (1, 64, 1, 0, 0), (7, 16, 100, 40, 100), (300, 8, 50, 20, 2000), (513, 32, 10, 3, 900),
+    (4, 16, 5000, 9000, 4000), (64, 128, 3000, 700, 5), (40, 8, 100, 100, 0), (1000, 1024, 5000, 3, 700),
+]
+
+
+@pytest.mark.parametrize("case", PLANS, ids=lambda c: "B%d_P%d_h%d_n%d_s%d" % c)
+@pytest.mark.parametrize("kind", ["grow", "mixed"])
+def test_plan(case, kind):
+    B, P, most, add, spare = case
+    rng = np.random.default_rng(sum(case) + (kind == "grow"))
+    held = rng.integers(0, most + 1, B)
+    if kind == "grow":
+        want = held + rng.integers(0, add + 1, B)
+    else:      # some end, some shrink, some grow, some stay
+        how = rng.integers(0, 4, B)
+        want = np.where(how == 0, 0, np.where(how == 1, rng.integers(0, held + 1), held + (how == 2) * rng.integers(0, add + 1, B)))
+    rows, free = start_pages(rng, held, P, sum(-(-int(h) // P) for h in held) + spare)
+    n_pages = sum(map(len, rows)) + len(free)
+    max_pages = max(1, -(-(most + add // 2) // P))       # some do not fit their row
+    max_pages = max(max_pages, max(map(len, rows)))
+    N = int(np.maximum(want - held, 0).sum()) + 5
+    table = table_of(rows, max_pages)
+    fl = dev_i32((free + [-7] * n_pages)[:max(n_pages, 1)])
+    count = dev_i32([len(free)])
+    n_pages = max(n_pages, 1)
+    ref = oracle.page_plan(held, want, {"rows": rows, "max_pages": max_pages}, free, P, N)
+    cu, granted, slots = run_plan(P, N, held, want, table, fl, count, n_pages)
+    assert granted == ref[1]
+    assert cu == ref[0]
+    assert slots == ref[2]
+    assert torch.equal(table, table_of(ref[3], max_pages))
+    assert count.tolist() == [len(ref[4])] and fl.tolist()[: len(ref[4])] == ref[4]
+    # giving back what the call took restores table and list, when it only took
+    if kind == "grow":
+        cu, back, slots = run_plan(P, 3, granted, held, table, fl, count, n_pages)
+        assert back == held.tolist() and cu == [0] * (B + 1) and slots == [-1] * 3
+        assert torch.equal(table, table_of(rows, max_pages))
+        assert count.tolist() == [len(free)] and fl.tolist()[: len(free)] == free
+
+
+def test_plan_no_requests():
+    sh = moda.make_paged_shape(0, 4, 1, 1, 128, 0, 16, 3, 2)
+    fl, count, cu = dev_i32([2, 0, 1]), dev_i32([3]), dev_i32([9])
+    slots = torch.zeros(4, dtype=torch.int64, device=DEV)
+    moda.moda_page_plan(sh, None, None, None, fl, count, cu, None, slots)
+    assert cu.tolist() == [0] and count.tolist() == [3] and slots.tolist() == [-1] * 4
+
+
+def bad_status():
+    with pytest.raises(moda.MoDAError) as err:
+        moda.moda_check_status()
+    assert err.value.status == moda.MODA_ERR_INVALID_ARG and "out of range" in str(err.value)
+    moda.moda_check_status()                       # the report clears it
+
+
+def test_plan_out_of_range_lengths():
+    """Lengths outside the table are cut, too many tokens for N get no slot;
+    both are reported and nothing outside the arrays is touched."""
+    P, mp = 8, 3
+    table = table_of([[0, 1, 2], []], mp)
+    fl, count = dev_i32([5, 4, 3, -1, -1, -1]), dev_i32([3])
+    cu, granted, slots = run_plan(P, 4, [100, -5], [24, 10], table, fl, count, 6)
+    bad_status()
+    assert granted == [24, 10] and cu == [0, 0, 10]          # held 100 counts as 24, -5 as 0
+    assert slots == [3 * 8, 3 * 8 + 1, 3 * 8 + 2, 3 * 8 + 3]
+    assert table.tolist() == [[0, 1, 2], [3, 4, -1]] and count.tolist() == [1]
+    # a free count beyond the cache counts as all its pages
+    table, fl, count = table_of([[]], mp), dev_i32([0, 1]), dev_i32([1 << 30])
+    cu, granted, slots = run_plan(P, 8, [0], [8], table, fl, count, 2)
+    bad_status()
+    assert granted == [8] and slots == list(range(8, 16)) and count.tolist() == [1]
+
+
+# --------------------------------------------------------------------- append --
+@pytest.mark.parametrize("N,Hk,d,P,dtype", [(1, 1, 64, 8, "bf16"), (5, 3, 64, 16, "fp32"), (257, 2, 128, 64, "bf16"),
+                                            (1000, 8, 128, 8, "fp32"), (4099, 5, 64, 1024, "bf16")])
+def test_append(N, Hk, d, P, dtype):
+    g = torch.Generator().manual_seed(N)
+    dt = torch_dtype(dtype)
+    n_pages = -(-N // P) + 3
+    k, v = (torch.randn(N, Hk, d, generator=g).to(dt) for _ in range(2))
+    k.view(-1)[0], v.view(-1)[-1] = float("nan"), float("-inf")        # bytes, whatever they say
+    slots = torch.randperm(n_pages * P, generator=g)[:N]
+    slots[::7] = -1
+    gd = Guarded()
+    kc, vc = (gd.empty(n, (n_pages, Hk, P, d), dt, DEV, output=False) for n in ("kc", "vc"))
+    kc.fill_(7.0), vc.fill_(-7.0)
+    sh = moda.make_paged_shape(1, N, Hk, Hk, d, 0, P, n_pages, 1, dtype=moda.MODA_FP32 if dtype == "fp32" else 0)
+    moda.moda_cache_append(sh, k.to(DEV), v.to(DEV), slots.to(DEV), kc, vc)
+    gd.check()
+    rk, rv = torch.full((n_pages, Hk, P, d), 7.0, dtype=dt), torch.full((n_pages, Hk, P, d), -7.0, dtype=dt)
+    at = slots >= 0
+    rk[slots[at] // P, :, slots[at] % P] = k[at]
+    rv[slots[at] // P, :, slots[at] % P] = v[at]
+    raw = torch.int32 if dtype == "fp32" else torch.int16
+    assert torch.equal(kc.cpu().view(raw), rk.view(raw)) and torch.equal(vc.cpu().view(raw), rv.view(raw))
+
+
+def test_append_out_of_range_slots():
+    sh = moda.make_paged_shape(1, 4, 1, 1, 64, 0, 8, 2, 1)
+    gd = Guarded()
+    kc, vc = (gd.empty(n, (2, 1, 8, 64), torch.bfloat16, DEV, output=False) for n in ("kc", "vc"))
+    kc.zero_(), vc.zero_()
+    k = torch.ones(4, 1, 64, dtype=torch.bfloat16, device=DEV)
+    moda.moda_cache_append(sh, k, k, torch.tensor([16, 1 << 40, -2, 15], device=DEV), kc, vc)
+    gd.check()
+    bad_status()
+    assert float(kc.float().sum()) == 64.0 and bool((kc[1, 0, 7] == 1).all())
+
+
+# ----------------------------------------------------------------------- mask --
+def run_mask(parent, cu, held, words, N):
+    B = len(cu) - 1
+    sh = moda.make_paged_shape(B, N, 1, 1, 128, 0, 16, 1, 1, words)
+    gd = Guarded()
+    mask, pos = gd.empty("mask", (N, words), torch.int32, DEV, output=False), gd.empty("pos", (N,), torch.int32, DEV, output=False)
+    mask.fill_(-9), pos.fill_(-9)
+    moda.moda_tree_mask(sh, dev_i32(parent), dev_i32(cu), None if held is None else dev_i32(held), mask, pos)
+    gd.check()
+    return mask.cpu(), pos.cpu()
+
+
+@pytest.mark.parametrize("new,words,pad", [((1,), 1, 0), ((32, 0, 33, 1), 2, 3), ((5, 7, 300), 10, 0), ((2048,), 64, 1),
+                                           ((0, 0), 1, 2), (tuple(range(64)), 3, 0)])
+@pytest.mark.parametrize("kind", ["random", "chain", "flat"])
+def test_mask(new, words, pad, kind):
+    rng = np.random.default_rng(len(new))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    N = int(cu[-1]) + pad
+    parent = {"random": random_parents(new, rng),
+              "chain": np.concatenate([np.arange(-1, n - 1) for n in new] + [[]]),
+              "flat": np.full(int(cu[-1]), -1)}[kind]
+    parent = np.concatenate([parent, np.full(pad, 77)]).astype(np.int32)
+    held = rng.integers(0, 1000, len(new))
+    see, rpos = oracle.tree_mask(parent, cu, held)
+    mask, pos = run_mask(parent, cu, held, words, N)
+    n = int(cu[-1])
+    assert torch.equal(mask[:n], mask_words(see, words)) and pos[:n].tolist() == rpos.tolist()
+    assert bool((mask[n:] == -9).all()) and bool((pos[n:] == -9).all())
+    _, pos0 = run_mask(parent, cu, None, words, N)
+    assert pos0[:n].tolist() == oracle.tree_mask(parent, cu)[1].tolist()
+
+
+def test_mask_out_of_range():
+    # a parent that is not earlier counts as the root; tokens behind 32*words get no row
+    mask, pos = run_mask([-1, 1, 0, -2, 5], [0, 5], [10], 1, 5)
+    bad_status()
+    assert mask[:, 0].tolist() == [1, 2, 5, 8, 16] and pos.tolist() == [10, 10, 11, 10, 10]
+    mask, pos = run_mask(list(range(-1, 39)), [0, 40], None, 1, 40)
+    bad_status()
+    assert pos[:32].tolist() == list(range(32)) and pos[32:].tolist() == [-9] * 8 and mask[32:].eq(-9).all()
+
+
+# ----------------------------------------------------------------------- tree --
+def run_tree(x, sh, stream=None, ws=None):
+    gd = Guarded()
+    n = moda.moda_tree_decode_workspace_size(sh)
+    if ws is None:
+        ws = gd.empty("ws", (max(n, 16),), torch.uint8, DEV, output=False)
+    o = gd.empty("o", tuple(x["q"].shape), x["q"].dtype, DEV, output=False)
+    lse = gd.empty("lse", tuple(x["q"].shape[:2]), torch.float32, DEV, output=False)
+    o.fill_(float("nan")), lse.fill_(float("nan"))
+    moda.moda_tree_decode(sh, x["q"], x["kc"], x["vc"], x["Kd"], x["Vd"], x["table"], x["held"], x["cu"], x["mask"],
+                          o, lse, ws, n, stream=stream)
+    gd.check()
+    return o, lse
+
+
+TREES = [
+    Tree(held=(1000,), new=(1,), chain=True),
+    Tree(held=(0,), new=(1,), L=0, chain=True),                        # nothing held: the token sees itself
+    Tree(held=(0, 5, 17), new=(3, 1, 9), L=3),
+    Tree(held=(127, 128, 129), new=(1, 2, 1), page=128),               # around a tile's end
+    Tree(held=(63, 64, 65, 200), new=(1, 1, 64, 0), page=64, chain=True),
+    Tree(held=(100, 0, 30), new=(0, 0, 5), L=48),                      # requests without new tokens
+    Tree(held=(300,), new=(33,), Hq=4, Hk=4, L=1),                     # G = 1
+    Tree(held=(300, 12), new=(33, 65), Hq=16, Hk=2, L=8, page=8),      # G = 8: several row tiles
+    Tree(held=(77,), new=(40,), Hq=6, Hk=2, L=5),                      # G = 3
+    Tree(held=(77, 3), new=(7, 2), Hq=64, Hk=1, L=6),                  # G = 64
+    Tree(held=(50,), new=(3,), Hq=40, Hk=2, L=2, d=64),                # G = 20
+    Tree(held=(700, 20, 4), new=(17, 31, 100), d=64, L=16, page=32),
+    Tree(held=(200, 50), new=(6, 10), L=130),                          # more depth rows than a tile
+    Tree(held=(200, 50), new=(6, 10), L=300, window=257, d=64),
+    Tree(held=(40, 9), new=(12, 3), L=48, window=5),
+    Tree(held=(2000,), new=(200,), chain=True, L=2, Hq=4, Hk=1),       # a chunk of a prompt
+    Tree(held=(0, 1), new=(150, 90), chain=True, L=0, page=8),         # prompts from nothing
+    Tree(held=(33, 500), new=(5, 8), pad=7, extra_words=2),
+    Tree(held=tuple(range(0, 400, 7)), new=tuple(1 + k % 3 for k in range(58)), Hq=4, Hk=2, L=4),
+    Tree(held=(3000, 10), new=(2, 2), page=1024, scale=0.3),
+    Tree(held=(513,), new=(64,), Hq=32, Hk=8, L=16),
+    Tree(held=(100, 20), new=(5, 9), dtype="fp32"),
+    Tree(held=(1000, 0, 64), new=(1, 1, 1), dtype="fp32", chain=True, d=64),
+    Tree(held=(300, 12), new=(33, 65), Hq=16, Hk=2, L=8, page=8, dtype="fp32"),
+    Tree(held=(200, 50), new=(6, 10), L=70, window=66, d=64, dtype="fp32"),
+    Tree(held=(50,), new=(9,), Hq=64, Hk=1, L=0, dtype="fp32", pad=2),
+]
+
+
+@pytest.mark.parametrize("c", TREES, ids=str)
+def test_tree(c):
+    x, see, sh = make_tree(c)
+    o, lse = run_tree(to_device(x), sh)
+    check_tree(c, x, see, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("held,L,n", [(0, 0, 40), (5, 0, 40), (0, 3, 9), (200, 2, 70)])
+def test_tree_any_mask(dtype, held, L, n):
+    """Masks that are no trees: rows without themselves, rows that see nothing
+    (with nothing held and no depth rows: o = 0, lse = -inf)."""
+    rng = np.random.default_rng(n)
+    c = Tree(held=(held,), new=(n,), L=L, dtype=dtype)
+    see = [rng.random((n, n)) < 0.2]
+    see[0][3] = False
+    see[0][n - 1] = False
+    x, see, sh = make_tree(c, see)
+    o, lse = run_tree(to_device(x), sh)
+    check_tree(c, x, see, o, lse)
+    if held == 0 and L == 0:
+        assert bool((o[3] == 0).all()) and bool(torch.isneginf(lse[3]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tree_not_finite_where_masked(dtype):
+    """Infinities and NaN in a drafted token's key and value, and in a token's
+    depth rows, reach the rows that see them and no others."""
+    inf, nan = float("inf"), float("nan")
+    c = Tree(held=(150, 20), new=(20, 9), L=4, dtype=dtype)
+    x, see, sh = make_tree(c)
+    at = lambda b, j: (int(x["table"][b][(c.held[b] + j) // c.page]), (c.held[b] + j) % c.page)  # noqa: E731
+    p, s = at(0, 7)
+    x["vc"][p, :, s, 3], x["vc"][p, 0, s, 90] = inf, nan
+    p, s = at(0, 11)
+    x["vc"][p, :, s, 3] = -inf
+    p, s = at(1, 4)
+    x["kc"][p, :, s] = nan                          # NaN scores where it is seen
+    x["Vd"][5, 1, 2, 10] = -inf
+    x["Kd"][25, 0, 1, 0] = nan
+    o, lse = run_tree(to_device(x), sh)
+    ref_finite = torch.isfinite(o[:29].float())
+    assert not bool(ref_finite.all()) and bool(ref_finite.any())
+    # rows with NaN scores are NaN in both; the others are compared
+    check_rows_not_finite(c, x, see, o, lse)
+
+
+def check_rows_not_finite(c, x, see, o, lse):
+    from paged_cases import oracle_tree
+    ref, rlse = oracle_tree(c, x, see)
+    clean = {k: (v.clone() if v is not None else None) for k, v in x.items()}
+    for k in ("vc", "Vd"):
+        clean[k][~torch.isfinite(clean[k].float())] = 0
+    a, _ = oracle_tree(c, clean, see, absolute=True)
+    n = int(x["cu"][-1])
+    o, lse = o.double().cpu().numpy()[:n], lse.double().cpu().numpy()[:n]
+    ref, rlse, a = ref[:n], rlse[:n], a[:n]
+    np.testing.assert_array_equal(np.isnan(o), np.isnan(ref))
+    np.testing.assert_array_equal(np.where(np.isinf(o), o, 0), np.where(np.isinf(ref), ref, 0))
+    fine = np.isfinite(ref)
+    assert (np.abs(o[fine] - ref[fine]) <= out_bound(c.dtype, ref[fine], a[fine])).all()
+    np.testing.assert_array_equal(np.isnan(lse), np.isnan(rlse))
+    seen = np.isfinite(rlse)
+    assert np.abs(lse[seen] - rlse[seen]).max() <= 1e-3
+
+
+def test_tree_bad_table_reads_as_zeros():
+    """A table entry that names no page: reported, read as zeros."""
+    c = Tree(held=(40,), new=(2,), L=0, chain=True)
+    x, see, sh = make_tree(c)
+    page = int(x["table"][0][1])
+    for bad in (-1, 1 << 30, sh.n_pages):
+        y = dict(x)
+        y["table"] = x["table"].clone()
+        y["table"][0][1] = bad
+        o, lse = run_tree(to_device(y), sh)
+        bad_status()
+        z = {k: (v.clone() if v is not None else None) for k, v in x.items()}
+        z["kc"][page], z["vc"][page] = 0, 0
+        check_tree(c, z, see, o, lse)
+
+
+def test_tree_out_of_range_lengths():
+    """Lengths beyond the table, N or the mask are cut and reported."""
+    c = Tree(held=(10, 10), new=(2, 2), L=0, page=16, chain=True)
+    x, see, sh = make_tree(c)
+    for held, cu in (([1 << 30, 10], [0, 2, 4]), ([10, -3], [0, 2, 4]), ([10, 10], [0, 2, 400]), ([10, 10], [0, 9, 4]),
+                     ([10, 10], [-4, 2, 4])):
+        y = dict(x)
+        y["table"] = y["table"].clamp(max=sh.n_pages - 1)
+        y["kc"], y["vc"] = torch.nan_to_num(x["kc"].float()).to(x["kc"].dtype), torch.nan_to_num(x["vc"].float()).to(x["vc"].dtype)
+        y["held"], y["cu"] = torch.tensor(held, dtype=torch.int32), torch.tensor(cu, dtype=torch.int32)
+        run_tree(to_device(y), sh)
+        bad_status()
+    c = Tree(held=(10,), new=(33,), L=0)
+    x, see, sh = make_tree(c)
+    sh.mask_words = 1
+    x["mask"] = x["mask"][:, :1].contiguous()
+    o, lse = run_tree(to_device(x), sh)
+    bad_status()
+    assert bool(torch.isnan(o[32]).all()) and not bool(torch.isnan(o[:32]).any())
+
+
+def test_tree_equals_decode():
+    """One new token a request over equal lengths: moda_decode's result."""
+    B, Hq, Hk, d, L, T, P = 3, 16, 4, 128, 5, 200, 16
+    c = Tree(held=(T - 1,) * B, new=(1,) * B, Hq=Hq, Hk=Hk, d=d, L=L, page=P, chain=True)
+    x, see, sh = make_tree(c)
+    y = to_device(x)
+    o, lse = run_tree(y, sh)
+    t = x["table"][:, : -(-T // P)].long()
+    K, V = (x[k][t].transpose(1, 2).reshape(B, Hk, -1, d)[:, :, :T].contiguous().to(DEV) for k in ("kc", "vc"))
+    ds = moda.make_shape(B, Hq, Hk, T, d, L, 0)
+    n = moda.moda_decode_workspace_size(ds)
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    moda.moda_decode(ds, y["q"], K, V, y["Kd"], y["Vd"], o2, lse2, torch.empty(n, dtype=torch.uint8, device=DEV), n)
+    assert (o.float() - o2.float()).abs().max() <= 2 ** -6 and (lse - lse2).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tree_deterministic_and_replayed(dtype):
+    """Equal bits again, in a graph, and in a graph replayed with other lengths."""
+    c = Tree(held=(900, 70, 333), new=(9, 30, 2), dtype=dtype, L=4)
+    x, see, sh = make_tree(c)
+    y = to_device(x)
+    o, lse = run_tree(y, sh)
+    o2, lse2 = run_tree(y, sh)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    n = moda.moda_tree_decode_workspace_size(sh)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    og, lg = torch.empty_like(o), torch.empty_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], y["mask"],
+                              og, lg, ws, n)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, og) and torch.equal(lse, lg)
+    c2 = Tree(held=(20, 800, 5), new=(9, 30, 2), dtype=dtype, L=4)
+    x2 = dict(x)
+    x2["held"] = torch.tensor(c2.held, dtype=torch.int32)
+    # the pages of request 1 as request 0 of the longer case: any pages do, if both sides read them
+    rows = torch.randint(0, sh.n_pages, x["table"].shape, generator=torch.Generator().manual_seed(4)).to(torch.int32)
+    x2["table"] = rows
+    x2["kc"], x2["vc"] = (torch.nan_to_num(x[k].float(), nan=0.5).to(x[k].dtype) for k in ("kc", "vc"))
+    for k in ("held", "table", "kc", "vc"):
+        y[k].copy_(x2[k])
+    og.fill_(float("nan")), lg.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    check_tree(c2, x2, see, og, lg)
+
+
+def test_tree_side_stream():
+    c = Tree(held=(400,), new=(12,))
+    x, see, sh = make_tree(c)
+    y = to_device(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    n = moda.moda_tree_decode_workspace_size(sh)
+    with torch.cuda.stream(s):
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        o, lse = torch.full_like(y["q"], float("nan")), torch.full(y["q"].shape[:2], float("nan"), device=DEV)
+    moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], y["mask"], o, lse,
+                          ws, n, stream=s)
+    s.synchronize()
+    check_tree(c, x, see, o, lse)
+
+
+def test_tree_workspace_too_small():
+    c = Tree(held=(40,), new=(2,))
+    x, _, sh = make_tree(c)
+    y = to_device(x)
+    n = moda.moda_tree_decode_workspace_size(sh)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    with pytest.raises(moda.MoDAError) as err:
+        moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], y["mask"],
+                              torch.empty_like(y["q"]), torch.empty(y["q"].shape[:2], device=DEV), ws, n - 1)
+    assert err.value.status == moda.MODA_ERR_WORKSPACE
+
+
+# ------------------------------------------------------------------- together --
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_speculative_steps(dtype):
+    """Prompts, then steps of draft, attention and acceptance over one cache:
+    plan, append, mask and attention of every step against the dense rows that
+    the accepted tokens leave."""
+    rng = np.random.default_rng(11)
+    g = torch.Generator().manual_seed(11)
+    dt = torch_dtype(dtype)
+    B, Hq, Hk, d, L, P, n_pages, max_pages = 3, 8, 2, 64, 3, 8, 60, 20
+    kc, vc = (torch.full((n_pages, Hk, P, d), float("nan"), dtype=dt, device=DEV) for _ in range(2))
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device=DEV)
+    fl, count = torch.randperm(n_pages, generator=g).to(torch.int32).to(DEV), dev_i32([n_pages])
+    held = dev_i32([0] * B)
+    dense = [[torch.zeros(0, Hk, d, dtype=dt) for _ in range(2)] for _ in range(B)]     # accepted keys, values
+    for step in range(5):
+        new = [int(n) for n in (rng.integers(20, 50, B) if step == 0 else rng.integers(0, 12, B))]
+        chain = step == 0
+        N = sum(new) + 2
+        parent = random_parents(new, rng)
+        cu_ref = np.concatenate([[0], np.cumsum(new)])
+        words = 0 if chain else 1
+        sh = moda.make_paged_shape(B, N, Hq, Hk, d, L, P, n_pages, max_pages, words,
+                                   moda.MODA_FP32 if dtype == "fp32" else moda.MODA_BF16)
+        cu, granted = torch.empty(B + 1, dtype=torch.int32, device=DEV), torch.empty(B, dtype=torch.int32, device=DEV)
+        slots = torch.empty(N, dtype=torch.int64, device=DEV)
+        moda.moda_page_plan(sh, held, held + dev_i32(new), table, fl, count, cu, granted, slots)
+        assert cu.tolist() == cu_ref.tolist() and granted.tolist() == (held + dev_i32(new)).tolist()
+        q, k, v = (torch.randn(N, h, d, generator=g).to(dt) for h in (Hq, Hk, Hk))
+        kd, vd = (torch.randn(N, Hk, L, d, generator=g).to(dt) for _ in range(2))
+        moda.moda_cache_append(sh, k.to(DEV), v.to(DEV), slots, kc, vc)
+        mask = None
+        see, pos_ref = oracle.tree_mask(parent, cu_ref, held.tolist())
+        if chain:
+            see = [np.tril(np.ones((n, n), bool)) for n in new]
+        else:
+            mask, pos = torch.zeros(N, 1, dtype=torch.int32, device=DEV), torch.zeros(N, dtype=torch.int32, device=DEV)
+            moda.moda_tree_mask(sh, dev_i32(np.concatenate([parent, [0, 0]])), cu, held, mask, pos)
+            assert pos.tolist()[: sum(new)] == pos_ref.tolist()
+        x = dict(q=q, kc=kc, vc=vc, Kd=kd, Vd=vd, table=table, held=held, cu=cu, mask=mask)
+        o, lse = run_tree(to_device(x), sh)
+        keep = []                      # the branch accepted of each request
+        for b in range(B):
+            c0 = int(cu_ref[b])
+            for i in range(new[b]):
+                path = c0 + np.nonzero(see[b][i])[0]
+                kk, vv = (torch.cat([dense[b][j], t[path]]).transpose(0, 1)[None] for j, t in ((0, k), (1, v)))
+                r, rl = oracle.decode(q[c0 + i][None].double(), kk.double(), vv.double(), kd[c0 + i][None].double(),
+                                      vd[c0 + i][None].double())
+                a, _ = oracle.decode(q[c0 + i][None].double(), kk.double(), vv.double().abs(), kd[c0 + i][None].double(),
+                                     vd[c0 + i][None].double().abs())
+                assert (np.abs(o[c0 + i].double().cpu().numpy() - r[0]) <= out_bound(dtype, r[0], a[0])).all()
+                assert np.abs(lse[c0 + i].double().cpu().numpy() - rl[0]).max() <= 1e-3
+            last = int(rng.integers(0, new[b])) if new[b] else -1
+            keep.append(np.arange(new[b]) if chain else (np.nonzero(see[b][last])[0] if new[b] else np.zeros(0, int)))
+        # the accepted tokens' rows again, at the slots of the positions they keep; the rest given back
+        order = torch.zeros(N, dtype=torch.int64)
+        at = slots.cpu().clone()
+        sl = torch.full((N,), -1, dtype=torch.int64)
+        for b in range(B):
+            c0 = int(cu_ref[b])
+            for j, i in enumerate(keep[b]):
+                order[c0 + j], sl[c0 + j] = c0 + int(i), at[c0 + j]
+            dense[b] = [torch.cat([dense[b][0], k[c0 + keep[b]]]), torch.cat([dense[b][1], v[c0 + keep[b]]])]
+        moda.moda_cache_append(sh, k[order].to(DEV), v[order].to(DEV), sl.to(DEV), kc, vc)
+        kept = held + dev_i32([len(p) for p in keep])
+        held2 = torch.empty_like(held)
+        moda.moda_page_plan(sh, granted, kept, table, fl, count, cu, held2, slots)
+        held = held2
+        assert held.tolist() == [x[0].shape[0] for x in dense]
+        assert int(count) == n_pages - sum(-(-h // P) for h in held.tolist())
