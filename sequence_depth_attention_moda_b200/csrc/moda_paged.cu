@@ -431,14 +431,22 @@ moda_status guarded(F&& f) noexcept {
 TreePlan tree_plan(const Paged& p) {
     TreePlan t;
     const int per = p.B > 0 ? (p.N + p.B - 1) / p.B : p.N;     // tokens of a request, on average
-    t.KT = 64;
-    t.rows = p.G <= 16 && static_cast<long long>(per) * p.G <= 16 ? 16 : 64;
-    t.sub = 1;
-    t.Tq = t.rows / p.G;
-    t.Tg = t.Tq * t.sub;
-    t.Lp = p.Lw > 0 ? p.Lw : 1;
-    t.dtok = t.Lp <= t.KT ? t.KT / t.Lp : 1;
-    t.dsplit = (t.Lp + t.KT - 1) / t.KT;
+    const int Lw = p.Lw > 0 ? p.Lw : 1;
+    if (p.elem_bytes == 2) {           // tensor cores: two 128-row tiles a job, one CTA an SM
+        t.rows = t.KT = 128;
+        t.Tq = t.rows / p.G;
+        t.Tg = 2 * t.Tq;
+        t.Lp = (Lw + 7) / 8 * 8;       // a token's depth rows begin on a swizzle atom
+        t.n_cta = device_sm_count();
+    } else {
+        t.KT = 64;
+        t.rows = p.G <= 16 && static_cast<long long>(per) * p.G <= 16 ? 16 : 64;
+        t.Tq = t.Tg = t.rows / p.G;
+        t.Lp = Lw;
+        t.n_cta = device_sm_count() * (t.rows == 64 && p.d == 128 ? 1 : 2);
+    }
+    t.dtok = Lw <= t.KT ? t.KT / t.Lp : 1;
+    t.dsplit = (Lw + t.KT - 1) / t.KT;
     const long long rows = static_cast<long long>(p.N) * p.G;
     t.rec_rows = rows < static_cast<long long>(t.Tg) * p.G ? static_cast<int>(rows) : t.Tg * p.G;
     t.n_cta = device_sm_count() * (t.rows == 64 && p.d == 128 ? 1 : 2);
@@ -594,7 +602,7 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         a.rec_rows = t.rec_rows; a.n_cta = t.n_cta; a.scale_log2 = p.scale_log2;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         phase_mark(0, s);
-        cudaError_t e = launch_tree_simt(p, t, a, s);
+        cudaError_t e = p.elem_bytes == 2 ? launch_tree_sm100(p, t, a, s) : launch_tree_simt(p, t, a, s);
         if (e == cudaSuccess) e = launch_tree_combine(p, t, a, s);
         if (e == cudaSuccess) phase_mark(1, s);
         return launched(e, "tree decode launch");

@@ -1,7 +1,7 @@
 // moda_tree.cuh -- what the two paths of the attention of drafted tokens over
 // a paged cache share: the arguments, the schedule, the visible sets and the
-// partial records (moda_tree_simt.cu: CUDA cores, fp32; moda_tree_sm100.cu:
-// tensor cores, bf16; moda_tree_combine.cu: merging split jobs).
+// partial records (moda_tree_simt.cu: CUDA cores, fp32, and the merging of split
+// jobs; moda_tree_sm100.cu: tensor cores, bf16).
 //
 // Work.  A job is (request b, KV head hk, group of Tg consecutive new tokens);
 // its rows are the G query heads of each token, row = token * G + head.  A job
@@ -340,12 +340,13 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // One path's plan for a shape: row tile and tile sizes, CTAs, workspace.
 struct TreePlan {
-    int rows, sub, KT;       // query rows per row tile, row tiles per job, keys per tile
+    int rows, KT;            // query rows per row tile, keys per tile
     int Tq, Tg, Lp, dtok, dsplit, rec_rows, n_cta;
     size_t off_ml, off_po, bytes;
 };
 TreePlan tree_plan(const Paged& p);
-cudaError_t launch_tree_simt(const Paged& p, const TreePlan& t, tree::TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_simt(const Paged& p, const TreePlan& t, const tree::TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_sm100(const Paged& p, const TreePlan& t, const tree::TreeArgs& a, cudaStream_t s);
 cudaError_t launch_tree_combine(const Paged& p, const TreePlan& t, const tree::TreeArgs& a, cudaStream_t s);
 
 }  // namespace moda

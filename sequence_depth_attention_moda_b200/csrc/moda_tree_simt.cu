@@ -1,5 +1,6 @@
 // moda_tree_simt.cu -- attention of drafted tokens over a paged cache on the
-// CUDA cores (the operator, the schedule and the masks: moda_tree.cuh).
+// CUDA cores, fp32 (the operator, the schedule and the masks: moda_tree.cuh),
+// and the merging of jobs that several CTAs share (both types).
 //
 // For one row (new token i of request b, query head h, KV head hk = h / G):
 //   s_k = scale <q, K_k>   over the keys k < held and the new keys the token sees
@@ -38,34 +39,13 @@ struct Lay {
     static constexpr int kBytes = kStart + static_cast<int>(sizeof(Start)) + 16;
 };
 
-template <typename E>
-__device__ __forceinline__ void load16(const E* p, float* v);
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float* v) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16(v.x, v.y), ptx::pack_bf16(v.z, v.w));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <typename E, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
     using L = Lay<D, R>;
     constexpr int DS = 64 / R;            // lanes sharing a 4x4 block
     constexpr int TPR = kThreads / R;     // softmax threads per row
-    constexpr int VE = 16 / static_cast<int>(sizeof(E));
     extern __shared__ __align__(16) unsigned char smem[];
     float* sq = reinterpret_cast<float*>(smem + L::kQ);
     float* sk = reinterpret_cast<float*>(smem + L::kK);
@@ -91,15 +71,15 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
         const int rows = j.ntok * a.G;
         __syncthreads();                  // the previous job is done with shared memory
         if (tid == 0) *spoison = 0;
-        for (int i = tid; i < R * (D / VE); i += kThreads) {
-            const int r = i / (D / VE), c = i % (D / VE) * VE;
-            float v[VE] = {};
+        for (int i = tid; i < R * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r < rows) {
                 const size_t row = static_cast<size_t>(j.r.cu0 + j.tok0 + r / a.G) * a.Hq + j.hk * a.G + r % a.G;
-                load16(static_cast<const E*>(a.q) + row * D + c, v);
+                v = load4(static_cast<const float*>(a.q) + row * D + c);
             }
-#pragma unroll
-            for (int e = 0; e < VE; ++e) sq[r * (D + 4) + c + e] = v[e] * a.scale_log2;
+            *reinterpret_cast<float4*>(&sq[r * (D + 4) + c]) =
+                make_float4(v.x * a.scale_log2, v.y * a.scale_log2, v.z * a.scale_log2, v.w * a.scale_log2);
         }
         float o[4][D / 64][4];
 #pragma unroll
@@ -144,32 +124,28 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
                 srow[tid] = off;
             }
             __syncthreads();
-            const E* kb = static_cast<const E*>(dep ? a.kd : a.kc);
-            const E* vb = static_cast<const E*>(dep ? a.vd : a.vc);
-#pragma unroll 4
-            for (int i = tid; i < kKeys * (D / VE); i += kThreads) {
-                const int r = i / (D / VE), c = i % (D / VE) * VE;
+            const float* kb = static_cast<const float*>(dep ? a.kd : a.kc);
+            const float* vb = static_cast<const float*>(dep ? a.vd : a.vc);
+#pragma unroll 8
+            for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), c = i % (D / 4) * 4;
                 const long long off = srow[r];
-                float kv[VE] = {}, vv[VE] = {};
+                float4 kv = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vv = kv;
                 if (off >= 0) {
-                    load16(kb + off + c, kv);
-                    load16(vb + off + c, vv);
+                    kv = load4(kb + off + c);
+                    vv = load4(vb + off + c);
                 }
                 if (r >= from) {
+                    float* e = &vv.x;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        if (!isfinite(vv[e])) {
-                            vv[e] = 0.0f;
+                    for (int k = 0; k < 4; ++k)
+                        if (!isfinite(e[k])) {
+                            e[k] = 0.0f;
                             *spoison = 1;
                         }
                 }
-#pragma unroll
-                for (int e = 0; e < VE; e += 4) {
-                    *reinterpret_cast<float4*>(&sk[r * (D + 4) + c + e]) =
-                        make_float4(kv[e], kv[e + 1], kv[e + 2], kv[e + 3]);
-                    *reinterpret_cast<float4*>(&sv[r * D + c + e]) =
-                        make_float4(vv[e], vv[e + 1], vv[e + 2], vv[e + 3]);
-                }
+                *reinterpret_cast<float4*>(&sk[r * (D + 4) + c]) = kv;
+                *reinterpret_cast<float4*>(&sv[r * D + c]) = vv;
             }
             __syncthreads();
             // S: 4 rows x 4 keys over this lane's share of the head dimension
@@ -294,9 +270,10 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         v[e] = o[r][c][e] * inv;
-                        if (poison) v[e] += not_finite_sum<E, D>(a, j, tk, col + e);
+                        if (poison) v[e] += not_finite_sum<float, D>(a, j, tk, col + e);
                     }
-                    store4(static_cast<E*>(a.o) + orow * D + col, make_float4(v[0], v[1], v[2], v[3]));
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * D + col) =
+                        make_float4(v[0], v[1], v[2], v[3]);
                 }
                 if (cg == 0) a.lse[orow] = row_lse(mr, lr);
             } else {
@@ -311,19 +288,13 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     }
 }
 
-template <typename E, int D, int R>
+template <int D, int R>
 cudaError_t launch_r(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
-    const void* f = reinterpret_cast<const void*>(tree_simt_kernel<E, D, R>);
+    const void* f = reinterpret_cast<const void*>(tree_simt_kernel<D, R>);
     const cudaError_t e = set_max_dynamic_smem(f, Lay<D, R>::kBytes);
     if (e != cudaSuccess) return e;
-    tree_simt_kernel<E, D, R><<<t.n_cta, kThreads, Lay<D, R>::kBytes, s>>>(a);
+    tree_simt_kernel<D, R><<<t.n_cta, kThreads, Lay<D, R>::kBytes, s>>>(a);
     return cudaGetLastError();
-}
-
-template <typename E>
-cudaError_t launch_t(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
-    if (p.d == 128) return t.rows == 16 ? launch_r<E, 128, 16>(t, a, s) : launch_r<E, 128, 64>(t, a, s);
-    return t.rows == 16 ? launch_r<E, 64, 16>(t, a, s) : launch_r<E, 64, 64>(t, a, s);
 }
 
 // Merges the records of a job that range ends cut: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
@@ -408,8 +379,9 @@ cudaError_t launch_combine(const TreePlan& t, const TreeArgs& a, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_tree_simt(const Paged& p, const TreePlan& t, TreeArgs& a, cudaStream_t s) {
-    return p.elem_bytes == 4 ? launch_t<float>(p, t, a, s) : launch_t<__nv_bfloat16>(p, t, a, s);
+cudaError_t launch_tree_simt(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
+    if (p.d == 128) return t.rows == 16 ? launch_r<128, 16>(t, a, s) : launch_r<128, 64>(t, a, s);
+    return t.rows == 16 ? launch_r<64, 16>(t, a, s) : launch_r<64, 64>(t, a, s);
 }
 
 cudaError_t launch_tree_combine(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
