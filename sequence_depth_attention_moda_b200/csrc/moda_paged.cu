@@ -432,19 +432,24 @@ TreePlan tree_plan(const Paged& p) {
     TreePlan t;
     const int per = p.B > 0 ? (p.N + p.B - 1) / p.B : p.N;     // tokens of a request, on average
     const int Lw = p.Lw > 0 ? p.Lw : 1;
-    if (p.elem_bytes == 2) {           // tensor cores: two 128-row tiles a job, one CTA an SM
+    t.tiles = 1;
+    if (p.elem_bytes == 2) {           // tensor cores: 128-row tiles, one CTA an SM
         t.rows = t.KT = 128;
         t.Tq = t.rows / p.G;
-        t.Tg = 2 * t.Tq;
+        // Two row tiles a job read the keys once for 256 rows, but leave two score
+        // buffers instead of three: for requests that fill one tile on average
+        // the one-tile kernel is faster (csrc/moda_tree_sm100.cu has the figures).
+        t.tiles = per > t.Tq ? 2 : 1;
         t.Lp = (Lw + 7) / 8 * 8;       // a token's depth rows begin on a swizzle atom
         t.n_cta = device_sm_count();
     } else {
         t.KT = 64;
         t.rows = p.G <= 16 && static_cast<long long>(per) * p.G <= 16 ? 16 : 64;
-        t.Tq = t.Tg = t.rows / p.G;
+        t.Tq = t.rows / p.G;
         t.Lp = Lw;
         t.n_cta = device_sm_count() * (t.rows == 64 && p.d == 128 ? 1 : 2);
     }
+    t.Tg = t.Tq * t.tiles;
     t.dtok = Lw <= t.KT ? t.KT / t.Lp : 1;
     t.dsplit = (Lw + t.KT - 1) / t.KT;
     const long long rows = static_cast<long long>(p.N) * p.G;

@@ -130,6 +130,7 @@ struct Start {
     long long warp_sum[32];
     long long x_total;
     int b, hk, group, i0;    // first job and the first tile within it
+    Request r;
     int count;               // tiles of this CTA
 };
 
@@ -189,6 +190,7 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
                 s->hk = hk;
                 s->group = g;
                 s->i0 = static_cast<int>(lo - at);
+                s->r = j.r;
                 s->count = static_cast<int>(hi - lo);
                 h.job_start = at;
                 h.nt = j.nt;
@@ -218,7 +220,7 @@ struct Walk {
         if (left <= 0) return false;
         j.b = s.b;
         j.hk = s.hk;
-        j.r = load_request(a, s.b);
+        j.r = s.r;
         set_group(a, j, s.group);
         take(s.i0);
         return true;
@@ -302,30 +304,38 @@ __device__ __forceinline__ int page_of(const TreeArgs& a, int b, int key) {
 // in a value that only some of a tile's query rows see would reach the others.
 // So in the rows of V that are masked for anybody (new keys, depth rows) such
 // elements are replaced by 0 before the product and the record is marked; the
-// (rare) marked rows add them back here, each from the keys it sees.  Added
-// without its weight: p > 0 does not change an infinity or a NaN.
+// (rare) marked rows add them here, to the outputs just stored and each from
+// the keys it sees.  Added without its weight: p > 0 does not change an
+// infinity or a NaN.
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Columns c0, c0 + step, ... (n of them) of output row `out`, stored before by the same thread.
 template <typename E, int D>
-__device__ __noinline__ float not_finite_sum(const TreeArgs& a, const Job& j, int token, int col) {
-    float sum = 0.0f;
-    auto add = [&](const E* p) {
-        const float v = to_float(*p);
-        if (!isfinite(v)) sum += v;
-    };
+__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Job j, int token, E* out, int c0, int step,
+                                            int n) {
     const int page = 1 << a.page_shift;
-    for (int k = 0; k < j.r.n; ++k) {
-        const int key = j.r.held + k;
-        if (!(seq_visible(a, j.r, token, key) & 1u)) continue;
-        const int p = page_of(a, j.b, key);
-        if (p < 0) continue;
-        add(static_cast<const E*>(a.vc) +
-            ((static_cast<size_t>(p) * a.Hk + j.hk) * page + (key & (page - 1))) * D + col);
-    }
     const size_t row = (static_cast<size_t>(j.r.cu0 + token) * a.Hk + j.hk) * a.L;
-    for (int l = a.win_lo; l < a.L; ++l) add(static_cast<const E*>(a.vd) + (row + l) * D + col);
-    return sum;
+    for (int x = 0; x < n; ++x) {
+        const int col = c0 + x * step;
+        float sum = to_float(out[col]);
+        auto add = [&](const E* p) {
+            const float v = to_float(*p);
+            if (!isfinite(v)) sum += v;
+        };
+        for (int k = 0; k < j.r.n; ++k) {
+            const int key = j.r.held + k;
+            if (!(seq_visible(a, j.r, token, key) & 1u)) continue;
+            const int p = page_of(a, j.b, key);
+            if (p < 0) continue;
+            add(static_cast<const E*>(a.vc) +
+                ((static_cast<size_t>(p) * a.Hk + j.hk) * page + (key & (page - 1))) * D + col);
+        }
+        for (int l = a.win_lo; l < a.L; ++l) add(static_cast<const E*>(a.vd) + (row + l) * D + col);
+        from_float(out + col, sum);
+    }
 }
 
 // A record's l is a sum of exponentials, never negative: its sign carries the
@@ -341,6 +351,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // One path's plan for a shape: row tile and tile sizes, CTAs, workspace.
 struct TreePlan {
     int rows, KT;            // query rows per row tile, keys per tile
+    int tiles;               // row tiles per job (1 or 2)
     int Tq, Tg, Lp, dtok, dsplit, rec_rows, n_cta;
     size_t off_ml, off_po, bytes;
 };

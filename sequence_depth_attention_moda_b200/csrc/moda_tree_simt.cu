@@ -266,14 +266,10 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     const int col = 4 * cg + 64 * c;
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] = o[r][c][e] * inv;
-                        if (poison) v[e] += not_finite_sum<float, D>(a, j, tk, col + e);
-                    }
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * D + col) =
-                        make_float4(v[0], v[1], v[2], v[3]);
+                    float* out = static_cast<float*>(a.o) + orow * D;
+                    *reinterpret_cast<float4*>(out + col) =
+                        make_float4(o[r][c][0] * inv, o[r][c][1] * inv, o[r][c][2] * inv, o[r][c][3] * inv);
+                    if (poison) add_not_finite<float, D>(a, j, tk, out, col, 1, 4);
                 }
                 if (cg == 0) a.lse[orow] = row_lse(mr, lr);
             } else {
@@ -315,8 +311,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     if (h.job_start >= range_begin(c, h.x_total, P) || h.job_start < prev) return;
     const long long end = h.job_start + h.nt;
     // records: range c-1 (slot 0 if the job is its first), then slot 0 of each range that begins inside the job
-    int n = 1;
-    while (c - 1 + n < P && range_begin(c - 1 + n, h.x_total, P) < end) ++n;
+    const int n = static_cast<int>((end * P - 1) / h.x_total) - c + 2;    // up to the range that holds tile end - 1
     auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(c - 1 + i) + (i == 0 && h.job_start > prev); };
     Job j;
     j.b = h.b;
@@ -349,13 +344,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
         const size_t orow = static_cast<size_t>(j.r.cu0 + tk) * a.Hq + j.hk * a.G + row % a.G;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int e = 0; e < C; ++e) {
-            float v = acc[e] * inv;
-            if (poison) v += not_finite_sum<E, D>(a, j, tk, lane + 32 * e);
-            E* dst = static_cast<E*>(a.o) + orow * D + lane + 32 * e;
-            if constexpr (sizeof(E) == 4) *dst = v;
-            else *dst = __float2bfloat16_rn(v);
-        }
+        for (int e = 0; e < C; ++e) from_float(static_cast<E*>(a.o) + orow * D + lane + 32 * e, acc[e] * inv);
+        if (poison) add_not_finite<E, D>(a, j, tk, static_cast<E*>(a.o) + orow * D, lane, 32, C);
         if (lane == 0) a.lse[orow] = row_lse(ref, l);
     }
 }

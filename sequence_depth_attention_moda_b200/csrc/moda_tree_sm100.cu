@@ -8,30 +8,30 @@
 // that few of their 128 rows are real; at R = 256 the two are about even.
 //
 // One CTA per SM over a contiguous range of the flattened list of 128-key
-// tiles, which it streams through a K ring and a V ring.  Two softmax
-// warpgroups ("streams") each own an S tile and an O accumulator in TMEM:
-//   a job of at most 128 rows   both streams hold the same query tile and take
-//                               the tiles alternately; their (m, l, O) are
-//                               merged at the end of the segment;
-//   a job of up to 256 rows     stream s holds query tile s and takes every
-//                               sequence tile, and its own tokens' depth tiles.
-// Either way each stream's chain scores -> softmax -> values of one tile runs
-// beside the other's, and a tile is loaded once for all rows of the job.
+// tiles, which it streams through a K ring and a V ring.  A job has one or two
+// query tiles of 128 rows; a block is one key tile against one query tile, and
+// a sequence tile is loaded once for both of a job's query tiles (two blocks),
+// a depth tile holds one query tile's tokens (one block).  Jobs of one query
+// tile use the two query slots (shared memory) and O accumulators (TMEM) in
+// turn, so a job's products start while the one before is written out.
 //
-// Warps: 0 TMA producer (Q, K, V; a lane a page or a token, so pages as small
-// as 8 rows cost one issue each); 1 clears the V rows that are not there and
-// the values that are not finite (below); 2 issues S = Q K^T; 3 issues
-// O += P V; 4..7 and 8..11 the streams' softmax, one thread a row: exponentials
-// against the running reference without a maximum, which is taken only when a
-// row sum passes 2^11 or a row has seen no key yet (exact: any reference gives
-// the same quotient), P in bf16 over the score columns.
-// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+d), O1 [384,384+d).
+// Warps: 0 TMA producer (Q, K; a lane a page or a token, so pages as small
+// as 8 rows cost one issue each); 1 TMA producer of V, which also clears the V
+// rows that are not there and the values that are not finite (below); 2 issues
+// S = Q K^T, up to the number of S buffers ahead; 3 issues O += P V; 4..11
+// softmax, 16 rows a warp and two threads a row (columns [0,64) and [64,128)): O
+// and l are rescaled only when the maximum passes the reference by more than
+// 2^8 (exact: any reference gives the same quotient), P in bf16 over the score
+// columns.  Warps without a real row,
+// and in depth tiles those whose tokens are not in the tile, skip the work.
+// TMEM columns: S buffers from 0 (two for d = 128, three for d = 64), then two
+// O accumulators of d.
 //
 // Warp 1: a tile that ends a request's keys leaves rows of the V stage unwritten
 // (pages behind the last key are not loaded) or with what the page held; P is
 // 0 there, but 0 * NaN is not, so it stores zeros.  In rows that only some of the
 // query rows see (new keys, depth rows) it replaces infinities and NaN and
-// marks the segment (not_finite_sum).  Tiles of held keys pass untouched.
+// marks the segment (add_not_finite).  Tiles of held keys pass untouched.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -46,36 +46,39 @@ using namespace tree;
 
 constexpr int kTile = 128;                   // keys per tile, rows per query tile
 constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
 constexpr uint32_t kSlab = 128 * 128;        // 128 rows x 64 bf16
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;
-constexpr float kSumLimit = 2048.0f;         // largest row sum of a tile kept without a new reference
+constexpr float kLazy = 8.0f;                // log2 by which a maximum may pass the reference
 constexpr int kMarks = 8;                    // segments whose marks are told apart
 
-template <int D>
+// NQ: query tiles of a job, and O accumulators.
+template <int D, int NQ>
 struct Lay {
     static constexpr int kSlabs = D / 64;
     static constexpr uint32_t kTileBytes = kSlabs * kSlab;
-    // V stages are held until P V is done, K stages only until S is
-    static constexpr int kKS = D == 128 ? 2 : 5;
-    static constexpr int kVS = D == 128 ? 3 : 6;
-    static constexpr uint32_t kQ = 0;                       // two query tiles
-    static constexpr uint32_t kK = 2 * kTileBytes;
+    // all of shared memory: V stages are held until P V is done, K stages only until S is
+    static constexpr int kKS = D == 128 ? (NQ == 1 ? 3 : 2) : (NQ == 1 ? 6 : 5);
+    static constexpr int kVS = D == 128 ? 3 : (NQ == 1 ? 7 : 6);
+    static constexpr int kNS = D == 128 && NQ == 2 ? 2 : 3;  // S buffers
+    static constexpr uint32_t kColO = kNS * 128;            // O of slot s: + s * D
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = NQ * kTileBytes;
     static constexpr uint32_t kV = kK + kKS * kTileBytes;
     static constexpr uint32_t kBar = kV + kVS * kTileBytes;
-    // barrier indexes
-    static constexpr int kQFull = 0, kQFree = 2, kKFull = 4, kKEmpty = kKFull + kKS, kVFull = kKEmpty + kKS,
-                         kVFix = kVFull + kVS, kVEmpty = kVFix + kVS, kSFull = kVEmpty + kVS, kPReady = kSFull + 2,
-                         kPVDone = kPReady + 2, kOFree = kPVDone + 2, kXDone = kOFree + 2, kNumBars = kXDone + 2;
-    static constexpr uint32_t kExch = kBar + (kNumBars * 8 + 15) / 16 * 16;   // float2 [128]
-    static constexpr uint32_t kStart = kExch + 128 * 8;
+    // barrier indexes; from kPReady on they take an arrival of each softmax warp
+    static constexpr int kQFull = 0, kQFree = NQ, kKFull = 2 * NQ, kKEmpty = kKFull + kKS, kVFull = kKEmpty + kKS,
+                         kVFix = kVFull + kVS, kVEmpty = kVFix + kVS, kSFull = kVEmpty + kVS, kSFree = kSFull + kNS,
+                         kOFull = kSFree + kNS, kPReady = kOFull + NQ, kOFree = kPReady + kNS, kNumBars = kOFree + NQ;
+    static constexpr uint32_t kStart = kBar + (kNumBars * 8 + 15) / 16 * 16;
     static constexpr uint32_t kMisc = kStart + (sizeof(Start) + 15) / 16 * 16;  // tmem base, abort flag, marks
     static constexpr uint32_t kBytes = kMisc + 16 + kMarks * 4;
     static constexpr uint32_t kDynSmem = kBytes + 1024;     // alignment slack
+    static_assert(kColO + NQ * D <= kTmemCols, "TMEM columns");
     static_assert(kDynSmem <= 232448, "shared memory of one CTA");
-    // warp 1 runs at most a V ring ahead of a segment's last tile, of which the
-    // two streams may still hold two
-    static_assert(kVS + 2 <= kMarks, "marks of segments in flight must differ");
+    // the softmax warps write out segment k before any P V of segment k+1 ends,
+    // so warp 1 is at most a V ring of tiles, each a segment, ahead of k
+    static_assert(kVS < kMarks, "marks of segments in flight must differ");
 };
 
 struct SmArgs {
@@ -84,42 +87,45 @@ struct SmArgs {
     int box_rows;        // rows of a cache box: min(page, 128)
 };
 
-// What every role derives alike while it walks the CTA's tiles.
+// What the MMA and softmax roles derive alike while they walk the CTA's tiles.
+// A slot is a query tile's place: shared memory for Q, TMEM for O.  Jobs of one
+// query tile take the slots in turn.
+template <int NQ>
 struct Roles {
     int j = 0;           // tiles so far: ring stages, barrier phases
-    int qtog = 0;        // query slot of the next one-tile job
-    int qn[2] = {0, 0};  // uses of each query slot so far
-    int primary;         // stream of the segment's first tile (one-tile jobs)
-    int slot;            // query slot (one-tile jobs)
+    int b = 0;           // blocks so far: S buffers, barrier phases
+    int turn = 0;        // slot of the next job of one query tile
+    int used0 = 0, used1 = 0;   // segments that used each slot so far
     bool two;            // two query tiles
+    int first;           // slots first .. last
+    int last;
     __device__ __forceinline__ void segment(const TreeArgs& a, const Walk& w) {
-        two = w.j.ntok > a.Tq;
-        primary = j & 1;
-        slot = qtog;
+        two = NQ == 2 && w.j.ntok > a.Tq;
+        first = two ? 0 : turn;
+        last = two ? 1 : turn;
     }
-    // Streams (bit mask) that take the job's tile i, which is tile j of the CTA.
-    __device__ __forceinline__ int streams(const Walk& w, int i) const {
-        if (!two) return 1 << (j & 1);
-        return i < w.j.nseq ? 3 : (i < w.j.nseq + w.j.ndep0 ? 1 : 2);
+    __device__ __forceinline__ int used(int s) const { return NQ == 2 && s ? used1 : used0; }
+    // Query tile of slot s.
+    __device__ __forceinline__ int sub(int s) const { return two ? s : 0; }
+    // Whether slot s takes the job's tile i.
+    __device__ __forceinline__ bool takes(const Walk& w, int i, int s) const {
+        return !two || i < w.j.nseq || (i >= w.j.nseq + w.j.ndep0) == (s == 1);
     }
-    __device__ __forceinline__ int query_slot(int s) const { return two ? s : slot; }
     __device__ __forceinline__ void end_segment() {
-        if (two) {
-            ++qn[0];
-            ++qn[1];
-        } else {
-            ++qn[slot];
-            qtog ^= 1;
+        used0 += first == 0;
+        if (NQ == 2) {
+            used1 += last == 1;
+            if (!two) turn ^= 1;
         }
     }
 };
 
-// Sequence keys of a job, and whether a tile has rows that are masked for
-// somebody or are not there.
+// Sequence keys of a job.
 __device__ __forceinline__ int job_keys(const TreeArgs& a, const Job& j) {
     return j.r.held + (a.mask ? j.r.n : j.tok0 + j.ntok);
 }
-// Depth tile index within its query tile, and that tile's tokens.
+// A depth tile's query tile, its index there, and a query tile's tokens.
+__device__ __forceinline__ int dep_sub(const Walk& w, int i) { return i >= w.j.nseq + w.j.ndep0 ? 1 : 0; }
 __device__ __forceinline__ int dep_index(const Walk& w, int i) {
     const int dt = i - w.j.nseq;
     return dt < w.j.ndep0 ? dt : dt - w.j.ndep0;
@@ -128,24 +134,134 @@ __device__ __forceinline__ int sub_tokens(const TreeArgs& a, const Job& j, int s
     return sub == 0 ? min(j.ntok, a.Tq) : j.ntok - a.Tq;
 }
 
+// Rows of tile i from its first on that its products have to cover.
+__device__ __forceinline__ int tile_rows(const TreeArgs& a, const Walk& w, int i) {
+    if (i < w.j.nseq) return min(kTile, job_keys(a, w.j) - i * kTile);
+    const int dt = dep_index(w, i);
+    if (a.Lw <= kTile) return min(a.dtok, sub_tokens(a, w.j, dep_sub(w, i)) - dt * a.dtok) * a.Lp;
+    return min(kTile, a.Lw - dt % a.dsplit * kTile);
+}
+
+// A lane's share of a tile's load: one box of a page, or of a token's depth rows.
+struct Box {
+    bool mine, dep;
+    int c1, c2, c3;      // coordinates (c0 is the slab)
+    int row;             // first row in the tile
+    uint32_t bytes;      // of the whole tile
+};
+__device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Walk& w, int i, int lane) {
+    Box x;
+    x.dep = i >= w.j.nseq;
+    x.mine = false;
+    x.c1 = x.c2 = x.c3 = x.row = 0;
+    if (!x.dep) {
+        const int key = i * kTile + lane * box_rows;
+        const int left = min(kTile, job_keys(a, w.j) - i * kTile);
+        x.mine = lane * box_rows < left;
+        x.bytes = ((left + box_rows - 1) / box_rows) * box_rows * 128u * slabs;
+        if (x.mine) {
+            const int p = page_of(a, w.j.b, key);
+            x.row = lane * box_rows;
+            x.c1 = key & ((1 << a.page_shift) - 1);
+            x.c2 = p < 0 ? -1 : p * a.Hk + w.j.hk;      // outside: the box reads as zeros
+        }
+        return x;
+    }
+    const int sub = dep_sub(w, i), dt = dep_index(w, i);
+    const int tok = w.j.r.cu0 + w.j.tok0 + sub * a.Tq;
+    x.c2 = w.j.hk;
+    if (a.Lw <= kTile) {
+        const int cnt = min(a.dtok, sub_tokens(a, w.j, sub) - dt * a.dtok);
+        x.mine = lane < cnt;
+        x.bytes = cnt * a.Lw * 128u * slabs;
+        x.row = lane * a.Lp;
+        x.c1 = a.win_lo;
+        x.c3 = tok + dt * a.dtok + lane;
+    } else {
+        x.mine = lane == 0;
+        x.bytes = kTile * 128u * slabs;                 // rows behind the last depth row read as zeros
+        x.c1 = a.win_lo + dt % a.dsplit * kTile;
+        x.c3 = tok + dt / a.dsplit;
+    }
+    return x;
+}
+
+// Clears the rows of a V stage that P V covers (up to the next 16) but that
+// are not there, and takes infinities and NaN out of the rows that are masked
+// for some query row (whole warp).  True if it found any.
 template <int D>
+__device__ __forceinline__ bool clean_values(const TreeArgs& a, const Walk& w, int i, unsigned char* stage, int lane) {
+    const bool dep = i >= w.j.nseq;
+    const int from = dep ? 0 : max(0, w.j.r.held - i * kTile);
+    if (from >= kTile) return false;
+    const int rows = tile_rows(a, w, i);
+    const int groups = (rows + 31) / 32;
+    bool bad = false;
+#pragma unroll 1
+    for (int k = from / 32; k < groups; ++k) {           // 32 rows at a time: a row is 8 chunks of 16 bytes a slab
+        const int mine = 32 * k + lane;
+        const bool real = mine < rows && !(dep && a.Lw <= kTile && mine % a.Lp >= a.Lw);
+        const uint32_t there = __ballot_sync(0xffffffffu, real);
+        const uint32_t masked = 32 * k >= from ? 0xffffffffu : 0xffffffffu << (from & 31);
+#pragma unroll 1
+        for (int x = 0; x < D / 64; ++x) {
+            uint4* p = reinterpret_cast<uint4*>(stage + x * kSlab) + 32 * 8 * k + lane;   // row 4u + lane/8, chunk lane%8
+            uint4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = p[32 * u];
+            uint32_t acc = 0u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int row = 4 * u + (lane >> 3);
+                if (!(there >> row & 1)) {
+                    p[32 * u] = make_uint4(0, 0, 0, 0);
+                } else if (masked >> row & 1) {
+                    acc = not_finite_acc(v[u].x, acc);
+                    acc = not_finite_acc(v[u].y, acc);
+                    acc = not_finite_acc(v[u].z, acc);
+                    acc = not_finite_acc(v[u].w, acc);
+                }
+            }
+            if (__any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0u)) {
+                bad = true;
+#pragma unroll 1
+                for (int u = 0; u < 8; ++u) {
+                    const int row = 4 * u + (lane >> 3);
+                    if (!(there & masked & (1u << row))) continue;
+                    uint4 y = p[32 * u];
+                    uint32_t* e = &y.x;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        if ((e[z] & 0x7f80u) == 0x7f80u) e[z] &= 0xffff0000u;
+                        if ((e[z] & 0x7f800000u) == 0x7f800000u) e[z] &= 0x0000ffffu;
+                    }
+                    p[32 * u] = y;
+                }
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    return bad;
+}
+
+template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_constant__ SmArgs g) {
-    using L = Lay<D>;
+    using L = Lay<D, NQ>;
     const TreeArgs& a = g.t;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-    float2* exch = reinterpret_cast<float2*>(smem + L::kExch);
     Start* start = reinterpret_cast<Start*>(smem + L::kStart);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* marks = reinterpret_cast<volatile int*>(tmem_holder + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // the combine kernel may be set up now; it waits for this grid on the device
+    griddep_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::kNumBars; ++i)
-            mbar_init(&bars[i], (i >= L::kPReady && i < L::kPVDone) || i >= L::kOFree ? 4 : 1);
+        for (int i = 0; i < L::kNumBars; ++i) mbar_init(&bars[i], i >= L::kPReady ? kSoftmaxWarps : 1);
         *abort_flag = 0;
         for (int i = 0; i < kMarks; ++i) marks[i] = 0;
         fence_mbarrier_init();
@@ -154,214 +270,167 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         tmem_alloc(tmem_holder, kTmemCols);
         tmem_relinquish();
     }
+    if (threadIdx.x == 64) {
+        prefetch_tmap(&g.tq);
+        prefetch_tmap(&g.tk);
+        prefetch_tmap(&g.tv);
+    }
     tc_fence_before();
     schedule(a, start);        // ends with a CTA barrier
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     auto wait = [&](int bar, uint32_t phase) -> bool { return mbar_wait(&bars[bar], phase & 1, a.status, abort_flag); };
     auto wait_all = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
-
-    Walk w;
-    Roles r;
-    if (warp == 0) {
-        // ---------------------------------------------------------- producer --
-        if (lane == 0) {
-            prefetch_tmap(&g.tq);
-            prefetch_tmap(&g.tk);
-            prefetch_tmap(&g.tv);
-            if (a.Lw > 0) {
-                prefetch_tmap(&g.tkd);
-                prefetch_tmap(&g.tvd);
+    // one box a lane: arms the stage's barrier for the whole tile, then loads
+    auto load_tile = [&](const Box& x, int full, unsigned char* stage, const TmaMap* seq, const TmaMap* depth) {
+        if (lane == 0) mbar_arrive_expect_tx(&bars[full], x.bytes);
+        __syncwarp();
+        if (x.mine) {
+            unsigned char* dst = stage + x.row * 128;
+#pragma unroll
+            for (int y = 0; y < L::kSlabs; ++y) {
+                if (x.dep) tma_load_4d(dst + y * kSlab, depth, &bars[full], y * 64, x.c1, x.c2, x.c3);
+                else tma_load_3d(dst + y * kSlab, seq, &bars[full], y * 64, x.c1, x.c2);
             }
         }
+    };
+    // Every load lands before the CTA retires (bounded by time only: these
+    // waits ignore the abort flag).
+    auto drain = [&](int full, int stages, int issued) {
+        int no_abort = 0;
+        for (int x = max(0, issued - stages); x < issued; ++x)
+            mbar_wait(&bars[full + x % stages], (x / stages) & 1, a.status, &no_abort);
+    };
+
+    Walk w;
+    Roles<NQ> r;
+    // 384 threads of 168 registers: 128 x 104 + 256 x 200
+    if (warp < 4) {
+    regs_dec<104>();
+    if (warp == 0) {
+        // ------------------------------------------------- producer of Q, K --
         const uint32_t q_bytes = L::kSlabs * 128u * a.Tq * a.G;
-        int issued_k = 0, issued_v = 0;
         bool ok = true;
         for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
             r.segment(a, w);
-            for (int sub = 0; sub < (r.two ? 2 : 1); ++sub) {
-                const int sl = r.query_slot(sub);
-                if (r.qn[sl] > 0 && !wait_all(L::kQFree + sl, r.qn[sl] - 1)) {
+            for (int s = r.first; s <= r.last; ++s) {
+                if (r.used(s) > 0 && !wait_all(L::kQFree + s, r.used(s) - 1)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars[L::kQFull + sl], q_bytes);
-                    for (int s = 0; s < L::kSlabs; ++s)
-                        tma_load_3d(smem + L::kQ + sl * L::kTileBytes + s * kSlab, &g.tq, &bars[L::kQFull + sl], s * 64,
-                                    w.j.hk * a.G, w.j.r.cu0 + w.j.tok0 + sub * a.Tq);
+                    mbar_arrive_expect_tx(&bars[L::kQFull + s], q_bytes);
+                    for (int x = 0; x < L::kSlabs; ++x)
+                        tma_load_3d(smem + L::kQ + s * L::kTileBytes + x * kSlab, &g.tq, &bars[L::kQFull + s], x * 64,
+                                    w.j.hk * a.G, w.j.r.cu0 + w.j.tok0 + r.sub(s) * a.Tq);
                 }
             }
-            for (int i = w.i0; ok && i < w.i1; ++i, ++r.j) {
-                // this lane's box: coordinates, first row of the tile, rows
-                bool mine = false;
-                int c1 = 0, c2 = 0, c3 = 0, row = 0;
-                uint32_t bytes;
-                const bool dep = i >= w.j.nseq;
-                if (!dep) {
-                    const int key = i * kTile + lane * g.box_rows;
-                    const int boxes = kTile / g.box_rows;
-                    const int left = min(kTile, job_keys(a, w.j) - i * kTile);
-                    mine = lane < boxes && lane * g.box_rows < left;
-                    bytes = ((left + g.box_rows - 1) / g.box_rows) * g.box_rows * 128u * L::kSlabs;
-                    if (mine) {
-                        const int p = page_of(a, w.j.b, key);
-                        row = lane * g.box_rows;
-                        c1 = key & ((1 << a.page_shift) - 1);
-                        c2 = p < 0 ? -1 : p * a.Hk + w.j.hk;      // outside: the box reads as zeros
-                    }
-                } else {
-                    const int sub = r.two && i >= w.j.nseq + w.j.ndep0 ? 1 : 0;
-                    const int dt = dep_index(w, i);
-                    const int tok = w.j.r.cu0 + w.j.tok0 + sub * a.Tq;
-                    c2 = w.j.hk;
-                    if (a.Lw <= kTile) {
-                        const int cnt = min(a.dtok, sub_tokens(a, w.j, sub) - dt * a.dtok);
-                        mine = lane < cnt;
-                        bytes = cnt * a.Lw * 128u * L::kSlabs;
-                        row = lane * a.Lp;
-                        c1 = a.win_lo;
-                        c3 = tok + dt * a.dtok + lane;
-                    } else {
-                        mine = lane == 0;
-                        bytes = kTile * 128u * L::kSlabs;         // rows behind the last depth row read as zeros
-                        c1 = a.win_lo + dt % a.dsplit * kTile;
-                        c3 = tok + dt / a.dsplit;
-                    }
-                }
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int ns = kv ? L::kVS : L::kKS;
-                    const int st = r.j % ns;
-                    const int full = (kv ? L::kVFull : L::kKFull) + st;
-                    if (r.j >= ns && !wait_all((kv ? L::kVEmpty : L::kKEmpty) + st, r.j / ns - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&bars[full], bytes);
-                    __syncwarp();
-                    if (kv) issued_v = r.j + 1;
-                    else issued_k = r.j + 1;
-                    if (mine) {
-                        unsigned char* dst = smem + (kv ? L::kV : L::kK) + st * L::kTileBytes + row * 128;
-#pragma unroll
-                        for (int s = 0; s < L::kSlabs; ++s) {
-                            if (dep)
-                                tma_load_4d(dst + s * kSlab, kv ? &g.tvd : &g.tkd, &bars[full], s * 64, c1, c2, c3);
-                            else
-                                tma_load_3d(dst + s * kSlab, kv ? &g.tv : &g.tk, &bars[full], s * 64, c1, c2);
-                        }
-                    }
-                }
-            }
-            r.end_segment();
-        }
-        // every load lands before the CTA retires (bounded by time only: these
-        // waits ignore the abort flag)
-        if (lane == 0) {
-            int no_abort = 0;
-            for (int s = 0; s < 2; ++s)
-                if (r.qn[s] > 0) mbar_wait(&bars[L::kQFull + s], (r.qn[s] - 1) & 1, a.status, &no_abort);
-            for (int x = max(0, issued_k - L::kKS); x < issued_k; ++x)
-                mbar_wait(&bars[L::kKFull + x % L::kKS], (x / L::kKS) & 1, a.status, &no_abort);
-            for (int x = max(0, issued_v - L::kVS); x < issued_v; ++x)
-                mbar_wait(&bars[L::kVFull + x % L::kVS], (x / L::kVS) & 1, a.status, &no_abort);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------- rows of V that are not there --
-        bool ok = true;
-        for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
-            r.segment(a, w);
+            if (!ok) break;
             for (int i = w.i0; i < w.i1; ++i, ++r.j) {
-                const int st = r.j % L::kVS;
-                if (!wait_all(L::kVFull + st, r.j / L::kVS)) {
+                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, lane);
+                const int st = r.j % L::kKS;
+                if (r.j >= L::kKS && !wait_all(L::kKEmpty + st, r.j / L::kKS - 1)) {
                     ok = false;
                     break;
                 }
-                const bool dep = i >= w.j.nseq;
-                const int from = dep ? 0 : max(0, w.j.r.held - i * kTile);
-                if (from < kTile) {
-                    const int there = job_keys(a, w.j) - i * kTile;   // sequence rows of the tile that exist
-                    int cnt = 0, last = 0;                            // depth: tokens, or rows of one token
-                    if (dep) {
-                        const int sub = r.two && i >= w.j.nseq + w.j.ndep0 ? 1 : 0;
-                        const int dt = dep_index(w, i);
-                        cnt = min(a.dtok, sub_tokens(a, w.j, sub) - dt * a.dtok);
-                        last = a.Lw - dt % a.dsplit * kTile;
-                    }
-                    bool bad = false;
-#pragma unroll
-                    for (int s = 0; s < L::kSlabs; ++s) {
-                        uint4* base = reinterpret_cast<uint4*>(smem + L::kV + st * L::kTileBytes + s * kSlab);
-#pragma unroll 4
-                        for (int x = from * 8 + lane; x < kTile * 8; x += 32) {
-                            const int row = x >> 3;
-                            bool real;
-                            if (!dep) real = row < there;
-                            else if (a.Lw <= kTile) real = row / a.Lp < cnt && row % a.Lp < a.Lw;
-                            else real = row < last;
-                            if (!real) {
-                                base[x] = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            const uint4 v = base[x];
-                            uint32_t e[4] = {v.x, v.y, v.z, v.w};
-                            bool hit = false;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
-                                if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu, hit = true;
-                            }
-                            if (hit) {
-                                base[x] = make_uint4(e[0], e[1], e[2], e[3]);
-                                bad = true;
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    if (__any_sync(0xffffffffu, bad) && lane == 0) marks[w.seg % kMarks] = w.seg + 1;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::kVFix + st]);
+                load_tile(x, L::kKFull + st, smem + L::kK + st * L::kTileBytes, &g.tk, &g.tkd);
             }
             r.end_segment();
         }
+        if (lane == 0) {
+            for (int s = 0; s < NQ; ++s)
+                if (r.used(s) > 0) drain(L::kQFull + s, 1, r.used(s));
+            drain(L::kKFull, L::kKS, r.j);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------- producer of V, rows not there ----
+        // Two walks over the tiles, the loads up to a ring ahead of the
+        // cleaning; whichever can go on does.
+        Walk wl;
+        int il = 0, jl = 0, ic = 0, jc = 0;
+        bool more_l = wl.begin(a, *start), more_c = w.begin(a, *start);
+        Box x;
+        if (more_l) {
+            il = wl.i0;
+            ic = w.i0;
+            x = tile_box(a, g.box_rows, L::kSlabs, wl, il, lane);
+        }
+        unsigned long long t0 = 0;
+        for (uint32_t spins = 0; more_c; ++spins) {
+            bool moved = false;
+            if (jc < jl && __all_sync(0xffffffffu, mbar_test(&bars[L::kVFull + jc % L::kVS], (jc / L::kVS) & 1))) {
+                const int st = jc % L::kVS;
+                const bool bad = clean_values<D>(a, w, ic, smem + L::kV + st * L::kTileBytes, lane);
+                if (bad && lane == 0) marks[w.seg % kMarks] = w.seg + 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::kVFix + st]);
+                ++jc;
+                if (++ic == w.i1) {
+                    more_c = w.next(a);
+                    ic = w.i0;
+                }
+                moved = true;
+            }
+            if (more_l && (jl < L::kVS || __all_sync(0xffffffffu, mbar_test(&bars[L::kVEmpty + jl % L::kVS],
+                                                                           (jl / L::kVS - 1) & 1)))) {
+                const int st = jl % L::kVS;
+                load_tile(x, L::kVFull + st, smem + L::kV + st * L::kTileBytes, &g.tv, &g.tvd);
+                ++jl;
+                if (++il == wl.i1) {
+                    more_l = wl.next(a);
+                    il = wl.i0;
+                }
+                if (more_l) x = tile_box(a, g.box_rows, L::kSlabs, wl, il, lane);
+                moved = true;
+            }
+            // bounded like every wait
+            if (moved) {
+                t0 = 0;
+            } else if ((spins & 63u) == 0u) {
+                const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer(), 0);
+                if (t0 == 0) t0 = now;
+                const bool late = now - t0 > kWaitTimeoutNs;
+                if (late && lane == 0) {
+                    atomicOr(a.status, kStatusTimeout);
+                    *abort_flag = 1;
+                }
+                if (__any_sync(0xffffffffu, late || *abort_flag)) break;
+            }
+        }
+        if (lane == 0) drain(L::kVFull, L::kVS, jl);
     } else if (warp == 2) {
         // ------------------------------------------------------ S = Q K^T -----
         if (elect_one()) {
             const uint32_t id = idesc_bf16(128, kTile, false, false);
             const uint64_t qd = desc_kmajor_sw128(smem_u32(smem + L::kQ));
             const uint64_t kd = desc_kmajor_sw128(smem_u32(smem + L::kK));
-            int js[2] = {0, 0};
             bool ok = true;
             for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
                 r.segment(a, w);
-                for (int sub = 0; ok && sub < (r.two ? 2 : 1); ++sub)
-                    ok = wait(L::kQFull + r.query_slot(sub), r.qn[r.query_slot(sub)]);
+                for (int s = r.first; ok && s <= r.last; ++s) ok = wait(L::kQFull + s, r.used(s));
                 for (int i = w.i0; ok && i < w.i1; ++i, ++r.j) {
                     const int st = r.j % L::kKS;
                     if (!(ok = wait(L::kKFull + st, r.j / L::kKS))) break;
-                    const int set = r.streams(w, i);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (!(set >> s & 1)) continue;
-                        // S_s holds P of the stream's last tile until its P V is done
-                        if (js[s] > 0 && !(ok = wait(L::kPVDone + s, js[s] - 1))) break;
+                    for (int s = r.first; s <= r.last; ++s) {
+                        if (!r.takes(w, i, s)) continue;
+                        // the buffer holds P of block b - kNS until its P V is done
+                        const int sb = r.b % L::kNS;
+                        if (r.b >= L::kNS && !(ok = wait(L::kSFree + sb, r.b / L::kNS - 1))) break;
                         tc_fence_after();
-                        const uint64_t q0 = qd + ((r.query_slot(s) * L::kTileBytes) >> 4);
+                        const uint64_t q0 = qd + ((s * L::kTileBytes) >> 4);
                         const uint64_t k0 = kd + ((st * L::kTileBytes) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
-                            umma_ss(tmem + s * 128, q0 + off, k0 + off, id, kk > 0 ? 1u : 0u);
+                            umma_ss(tmem + sb * 128, q0 + off, k0 + off, id, kk > 0 ? 1u : 0u);
                         }
-                        umma_commit(&bars[L::kSFull + s]);
-                        ++js[s];
+                        umma_commit(&bars[L::kSFull + sb]);
+                        ++r.b;
                     }
                     if (ok) umma_commit(&bars[L::kKEmpty + st]);
                 }
                 if (ok)
-                    for (int sub = 0; sub < (r.two ? 2 : 1); ++sub) umma_commit(&bars[L::kQFree + r.query_slot(sub)]);
+                    for (int s = r.first; s <= r.last; ++s) umma_commit(&bars[L::kQFree + s]);
                 r.end_segment();
             }
         }
@@ -371,251 +440,223 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         if (elect_one()) {
             const uint32_t id = idesc_bf16(128, D, false, true);
             const uint64_t vd = desc_mnmajor_sw128(smem_u32(smem + L::kV), kSlab);
-            int js[2] = {0, 0}, segs[2] = {0, 0};
             bool ok = true;
             for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
                 r.segment(a, w);
-                int in_seg[2] = {0, 0};
+                // the slots' accumulators must have been read out
+                for (int s = r.first; ok && s <= r.last; ++s)
+                    if (r.used(s) > 0) ok = wait(L::kOFree + s, r.used(s) - 1);
+                int begun = 0;                        // slots with a product in this segment (bits)
                 for (int i = w.i0; ok && i < w.i1; ++i, ++r.j) {
                     const int st = r.j % L::kVS;
+                    const int steps = (tile_rows(a, w, i) + 15) / 16;     // 16 keys each
                     if (!(ok = wait(L::kVFix + st, r.j / L::kVS))) break;
-                    const int set = r.streams(w, i);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (!(set >> s & 1)) continue;
-                        // the first product of a segment overwrites O, which must have been read out
-                        if (in_seg[s] == 0 && segs[s] > 0 && !(ok = wait(L::kOFree + s, segs[s] - 1))) break;
-                        if (!(ok = wait(L::kPReady + s, js[s]))) break;
+                    for (int s = r.first; s <= r.last; ++s) {
+                        if (!r.takes(w, i, s)) continue;
+                        const int sb = r.b % L::kNS;
+                        if (!(ok = wait(L::kPReady + sb, r.b / L::kNS))) break;
                         tc_fence_after();
                         const uint64_t v0 = vd + ((st * L::kTileBytes) >> 4);
+                        if (steps == kTile / 16) {
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            umma_ts(tmem + kColO + s * 128, tmem + s * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
-                                    in_seg[s] > 0 || kk > 0 ? 1u : 0u);
-                        umma_commit(&bars[L::kPVDone + s]);
-                        ++js[s];
-                        ++in_seg[s];
+                            for (int kk = 0; kk < kTile / 16; ++kk)
+                                umma_ts(tmem + L::kColO + s * D, tmem + sb * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
+                                        (begun >> s & 1) || kk > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk < steps; ++kk)
+                                umma_ts(tmem + L::kColO + s * D, tmem + sb * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
+                                        (begun >> s & 1) || kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&bars[L::kSFree + sb]);
+                        begun |= 1 << s;
+                        ++r.b;
                     }
                     if (ok) umma_commit(&bars[L::kVEmpty + st]);
                 }
-                segs[0] += in_seg[0] > 0;
-                segs[1] += in_seg[1] > 0;
+                if (ok)
+                    for (int s = r.first; s <= r.last; ++s) umma_commit(&bars[L::kOFull + s]);
                 r.end_segment();
             }
         }
         __syncwarp();
+    }
     } else {
         // ------------------------------------------------------ softmax -------
-        const int s = (warp - 4) >> 2;               // stream
-        const int quarter = warp & 3;                // TMEM lanes 32*quarter ..
-        const int row = quarter * 32 + lane;
-        const int t_off = row / a.G;                 // token within the query tile
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint32_t s_col = lane_base + s * 128;
+        regs_inc<200>();
+        const int quarter = warp & 3;                 // TMEM lanes 32*quarter ..
+        const int half = lane >> 4;                   // column half of the row
+        const int row0 = quarter * 32 + ((warp - 4) >> 2) * 16;     // the warp's 16 rows
+        const int row = row0 + (lane & 15);
+        const int t_off = row / a.G;                  // token within the query tile
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(row0) << 16);
         const float sl2 = a.scale_log2;
-        int js = 0, merges[2] = {0, 0};              // tiles of this stream; merges with each secondary stream
         bool ok = true;
         for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
             r.segment(a, w);
-            const int sub = r.two ? s : 0;
-            const int n_tok = sub_tokens(a, w.j, sub);
-            const bool real = t_off < n_tok && t_off < a.Tq;
-            const bool active = quarter * 32 < n_tok * a.G;     // some row of the warp is real
-            const int token = w.j.tok0 + sub * a.Tq + t_off;    // relative to the request
-            float m = -INFINITY, l = 0.0f;
-            int in_seg = 0;
-            for (int i = w.i0; i < w.i1; ++i, ++r.j) {
-                if (!(r.streams(w, i) >> s & 1)) continue;
-                if (!wait_all(L::kSFull + s, js)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (active) {
-                    const bool dep = i >= w.j.nseq;
-                    const bool masked = dep || (i + 1) * kTile > w.j.r.held;
-                    const int dt = dep ? dep_index(w, i) : 0;
-                    // 32 scores from column 32c on; those the row does not see become -inf
-                    auto hide = [&](uint32_t* x, int c) {
-                        const uint32_t vis = !real ? 0xffffffffu
-                                                   : (dep ? dep_visible(a, t_off, dt, 32 * c)
-                                                          : seq_visible(a, w.j.r, token, i * kTile + 32 * c));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(vis >> e & 1)) x[e] = __float_as_uint(-INFINITY);
-                    };
-                    uint32_t pk[64];
-                    // p = 2^(s sl2 - ref), packed; returns the row sum
-                    auto exps = [&](float ref) -> float {
-                        float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        uint32_t x[2][32];
-                        tmem_ld32(s_col, x[0]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_wait_ld();
-                            reg_fence<32>(x[c & 1]);
-                            if (c < 3) tmem_ld32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
-                            if (masked) hide(x[c & 1], c);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float p0 = ex2(fmaf(__uint_as_float(x[c & 1][2 * e]), sl2, -ref));
-                                const float p1 = ex2(fmaf(__uint_as_float(x[c & 1][2 * e + 1]), sl2, -ref));
-                                rs[e & 3] += p0 + p1;
-                                pk[16 * c + e] = pack_bf16(p0, p1);
-                            }
-                        }
-                        return (rs[0] + rs[1]) + (rs[2] + rs[3]);
-                    };
-                    float rs = 0.0f;
-                    bool anew = __any_sync(0xffffffffu, real && m == -INFINITY);   // a row without a reference
-                    if (!anew) {
-                        rs = exps(real ? m : 0.0f);
-                        anew = __any_sync(0xffffffffu, real && !(rs <= kSumLimit));
-                    }
-                    if (anew) {
-                        float mx = -INFINITY;
+            // per slot (selects, so that they stay in registers); l: this half's share
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+            int prev0 = -1, prev1 = -1;               // the slot's last block in this segment
+            for (int i = w.i0; ok && i < w.i1; ++i) {
+                const bool dep = i >= w.j.nseq;
+                const bool masked = dep || (i + 1) * kTile > w.j.r.held;
+                const int dt = dep ? dep_index(w, i) : 0;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(s_col + 32 * c, x);
-                            tmem_wait_ld();
-                            reg_fence<32>(x);
-                            if (masked) hide(x, c);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                mx = fmax3(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                        }
-                        const float mn = fmaxf(m, mx * sl2);
-                        const float alpha = m == -INFINITY ? 1.0f : ex2(m - mn);   // o and l are 0 until a key is seen
-                        l *= alpha;
-                        m = mn;
-                        if (in_seg > 0) {
-                            // O holds the sum up to the last tile: its product was done before these scores began
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(lane_base + kColO + s * 128 + c, o);
-                                tmem_wait_ld();
-                                reg_fence<32>(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                tmem_st32(lane_base + kColO + s * 128 + c, o);
-                            }
-                            tmem_wait_st();
-                        }
-                        rs = exps(real && m != -INFINITY ? m : 0.0f);
-                    }
-                    l += rs;
-                    __syncwarp();
-                    tmem_st32(s_col, pk);
-                    tmem_st32(s_col + 32, pk + 32);
-                    tmem_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::kPReady + s]);
-                ++js;
-                ++in_seg;
-            }
-            if (!ok) break;
-            // ------------------------------------------------ end of segment --
-            // One query tile and two tiles or more: the other stream has a share.
-            const bool both = !r.two && w.i1 - w.i0 >= 2;
-            const bool second = both && s != r.primary;
-            if (in_seg > 0) {
-                if (!wait_all(L::kPVDone + s, js - 1)) {
-                    ok = false;
-                    break;
-                }
-                if (second) {
-                    exch[row] = make_float2(m, l);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[L::kXDone + s]);
-                } else {
-                    float m2 = -INFINITY, l2 = 0.0f;
-                    if (both) {
-                        if (!wait_all(L::kXDone + (s ^ 1), merges[s ^ 1])) {
-                            ok = false;
-                            break;
-                        }
-                        const float2 x = exch[row];
-                        m2 = x.x;
-                        l2 = x.y;
+                for (int s = r.first; s <= r.last; ++s) {
+                    if (!r.takes(w, i, s)) continue;
+                    const int sb = r.b % L::kNS;
+                    if (!wait_all(L::kSFull + sb, r.b / L::kNS)) {
+                        ok = false;
+                        break;
                     }
                     tc_fence_after();
-                    const float M = fmaxf(m, m2);
-                    const float w1 = m == -INFINITY ? 0.0f : ex2(m - M), w2 = m2 == -INFINITY ? 0.0f : ex2(m2 - M);
-                    const float lt = l * w1 + l2 * w2;
-                    const bool poison = marks[w.seg % kMarks] == w.seg + 1;
-                    const bool whole = w.whole();
-                    const float inv = !whole ? 1.0f : (lt == 0.0f ? 0.0f : 1.0f / lt);
-                    const float f1 = w1 * inv, f2 = w2 * inv;
-                    const size_t orow =
-                        static_cast<size_t>(w.j.r.cu0 + token) * a.Hq + w.j.hk * a.G + (row - t_off * a.G);
-                    const size_t rec = static_cast<size_t>(w.slot(a)) * a.rec_rows + sub * a.Tq * a.G + row;
-                    if (active) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(lane_base + kColO + s * 128 + c, o);
+                    const uint32_t s_addr = lane_base + sb * 128;
+                    float m = s ? m1 : m0, l = s ? l1 : l0;
+                    const int prev = s ? prev1 : prev0;
+                    const int n_tok = sub_tokens(a, w.j, r.sub(s));
+                    const bool real = t_off < n_tok && t_off < a.Tq;
+                    if (row0 < n_tok * a.G) {         // some row of the warp is real
+                        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};   // of this thread's 64 columns
+                        if (masked && real) {
+                            const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                vis[h] = dep ? dep_visible(a, t_off, dt, half * 64 + 32 * h)
+                                             : seq_visible(a, w.j.r, token, i * kTile + half * 64 + 32 * h);
+                        }
+                        uint32_t pk[32];
+                        if (dep && !__any_sync(0xffffffffu, real && (vis[0] | vis[1]))) {
+                            // none of the warp's tokens is in this tile
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) pk[e] = 0u;
+                        } else {
+                            uint32_t x[64];
+                            tmem_ld16x2_32<64>(s_addr, x);
+                            tmem_ld16x2_32<64>(s_addr + 32, x + 32);
                             tmem_wait_ld();
-                            reg_fence<32>(o);
-                            if (both) {
-                                uint32_t o2[32];
-                                tmem_ld32(lane_base + kColO + (s ^ 1) * 128 + c, o2);
-                                tmem_wait_ld();
-                                reg_fence<32>(o2);
+                            reg_fence<64>(x);
+                            if (masked) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f1 + __uint_as_float(o2[e]) * f2);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f1);
+                                for (int e = 0; e < 64; ++e)
+                                    if (!(vis[e >> 5] >> (e & 31) & 1)) x[e] = __float_as_uint(-INFINITY);
                             }
-                            if (!real) continue;
-                            if (whole) {
-                                if (poison) {
-#pragma unroll 1
-                                    for (int e = 0; e < 32; ++e) {
-                                        const float add = not_finite_sum<__nv_bfloat16, D>(a, w.j, token, c + e);
-                                        // o stays in registers: a select per element
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                                        for (int k = 0; k < 32; ++k)
-                                            if (k == e) o[k] = __float_as_uint(__uint_as_float(o[k]) + add);
+                            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    mx[u] = fmax3(mx[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+                            float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16)) * sl2;
+                            // a new reference (a row's first: m = -inf)
+                            if (__any_sync(0xffffffffu, real && mn > m + kLazy)) {
+                                mn = fmaxf(m, mn);
+                                // o and l are 0 until a key is seen
+                                const float alpha = m == -INFINITY ? 1.0f : ex2(m - mn);
+                                l *= alpha;
+                                m = mn;
+                                if (prev >= 0) {
+                                    // O must hold the sum up to the slot's last block.  Blocks up to b - kNS are
+                                    // done (their buffer's reuse waited for them); a later one's barrier can
+                                    // not have moved on, since the next use of its buffer needs a later P.
+                                    if (prev > r.b - L::kNS &&
+                                        !wait_all(L::kSFree + prev % L::kNS, prev / L::kNS)) {
+                                        ok = false;
+                                        break;
                                     }
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int c = 0; c < D / 2; c += 32) {
+                                        uint32_t o[32];
+                                        const uint32_t at = lane_base + L::kColO + s * D + c;
+                                        tmem_ld16x2_32<D / 2>(at, o);
+                                        tmem_wait_ld();
+                                        reg_fence<32>(o);
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                        tmem_st16x2_32<D / 2>(at, o);
+                                    }
+                                    tmem_wait_st();
                                 }
-                                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + c);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8)
-                                    dst[e / 8] = make_uint4(
-                                        pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                        pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                                        pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                                        pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-                            } else {
-                                uint4* dst = reinterpret_cast<uint4*>(a.po + rec * D + c);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4) dst[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                             }
+                            // p = 2^(s sl2 - m), packed
+                            const float ref = m == -INFINITY ? 0.0f : m;     // a row that sees nothing yet: p = 0
+                            float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float p0 = ex2(fmaf(__uint_as_float(x[2 * e]), sl2, -ref));
+                                const float p1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), sl2, -ref));
+                                rs[e & 3] += p0 + p1;
+                                pk[e] = pack_bf16(p0, p1);
+                            }
+                            l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
                         }
-                        if (real) {
-                            if (whole) a.lse[orow] = row_lse(M, lt);
-                            else a.ml[rec] = make_float2(M, poison ? -lt : lt);
-                        }
+                        __syncwarp();
+                        tmem_st16x2_32<32>(s_addr, pk);
+                        tmem_wait_st();
                     }
-                    // O (of both streams) may be overwritten
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bars[L::kOFree + s]);
-                        if (both) mbar_arrive(&bars[L::kOFree + (s ^ 1)]);
-                    }
+                    if (lane == 0) mbar_arrive(&bars[L::kPReady + sb]);
+                    const int blk = r.b++;
+                    if (s) m1 = m, l1 = l, prev1 = blk;
+                    else m0 = m, l0 = l, prev0 = blk;
                 }
             }
-            if (in_seg == 0 && r.two && real)    // two query tiles, and only depth tiles of the other one here
-                a.ml[static_cast<size_t>(w.slot(a)) * a.rec_rows + sub * a.Tq * a.G + row] = make_float2(-INFINITY, 0.0f);
-            if (both) ++merges[r.primary ^ 1];
+            // ------------------------------------------------ end of segment --
+            const bool whole = w.whole();
+#pragma unroll 1
+            for (int s = r.first; ok && s <= r.last; ++s) {
+                if (!wait_all(L::kOFull + s, r.used(s))) {
+                    ok = false;
+                    break;
+                }
+                const float m = s ? m1 : m0, l = s ? l1 : l0;
+                tc_fence_after();
+                const int n_tok = sub_tokens(a, w.j, r.sub(s));
+                const bool real = t_off < n_tok && t_off < a.Tq;
+                const bool poison = marks[w.seg % kMarks] == w.seg + 1;
+                const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
+                const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
+                const size_t orow = static_cast<size_t>(w.j.r.cu0 + token) * a.Hq + w.j.hk * a.G + (row - t_off * a.G);
+                const size_t rec = static_cast<size_t>(w.slot(a)) * a.rec_rows + r.sub(s) * a.Tq * a.G + row;
+                const bool some = row0 < n_tok * a.G && (s ? prev1 : prev0) >= 0;    // O of these rows was written
+                uint32_t o[D / 2];
+                if (some) {
+#pragma unroll
+                    for (int c = 0; c < D / 2; c += 32) tmem_ld16x2_32<D / 2>(lane_base + L::kColO + s * D + c, o + c);
+                    tmem_wait_ld();
+                    reg_fence<D / 2>(o);
+                }
+                // O is in registers: the slot's next job may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::kOFree + s]);
+                if (!real) continue;
+                if (whole) {
+                    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + orow * D;
+                    uint4* dst = reinterpret_cast<uint4*>(out + half * (D / 2));
+#pragma unroll
+                    for (int c = 0; c < D / 2; c += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[c + e]) * inv;
+                        dst[c / 8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                pack_bf16(v[6], v[7]));
+                    }
+                    if (poison) add_not_finite<__nv_bfloat16, D>(a, w.j, token, out, half * (D / 2), 1, D / 2);
+                    if (half == 0) a.lse[orow] = row_lse(m, lt);
+                } else {
+                    if (some) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.po + rec * D + half * (D / 2));
+#pragma unroll
+                        for (int c = 0; c < D / 2; c += 4) dst[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                    // a slot without a block here (only depth tiles of the other one): an empty record
+                    if (half == 0) a.ml[rec] = make_float2(m, poison ? -lt : lt);
+                }
+            }
             r.end_segment();
         }
     }
@@ -627,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
     }
 }
 
-template <int D>
+template <int D, int NQ>
 cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
     SmArgs g;
     g.t = a;
@@ -651,16 +692,17 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
         g.tkd = g.tk;
         g.tvd = g.tv;
     }
-    const void* f = reinterpret_cast<const void*>(tree_sm100_kernel<D>);
-    if ((e = set_max_dynamic_smem(f, Lay<D>::kDynSmem)) != cudaSuccess) return e;
-    tree_sm100_kernel<D><<<t.n_cta, kThreads, Lay<D>::kDynSmem, s>>>(g);
+    const void* f = reinterpret_cast<const void*>(tree_sm100_kernel<D, NQ>);
+    if ((e = set_max_dynamic_smem(f, Lay<D, NQ>::kDynSmem)) != cudaSuccess) return e;
+    tree_sm100_kernel<D, NQ><<<t.n_cta, kThreads, Lay<D, NQ>::kDynSmem, s>>>(g);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tree_sm100(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
-    return p.d == 128 ? launch_d<128>(p, t, a, s) : launch_d<64>(p, t, a, s);
+    if (p.d == 128) return t.tiles == 1 ? launch_d<128, 1>(p, t, a, s) : launch_d<128, 2>(p, t, a, s);
+    return t.tiles == 1 ? launch_d<64, 1>(p, t, a, s) : launch_d<64, 2>(p, t, a, s);
 }
 
 }  // namespace moda
