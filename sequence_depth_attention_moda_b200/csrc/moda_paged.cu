@@ -454,7 +454,6 @@ TreePlan tree_plan(const Paged& p) {
     t.dsplit = (Lw + t.KT - 1) / t.KT;
     const long long rows = static_cast<long long>(p.N) * p.G;
     t.rec_rows = rows < static_cast<long long>(t.Tg) * p.G ? static_cast<int>(rows) : t.Tg * p.G;
-    t.n_cta = device_sm_count() * (t.rows == 64 && p.d == 128 ? 1 : 2);
     t.off_ml = round256(sizeof(tree::CtaHeader) * t.n_cta);
     t.off_po = t.off_ml + round256(sizeof(float2) * 2 * t.n_cta * t.rec_rows);
     t.bytes = t.off_po + round256(sizeof(float) * 2 * t.n_cta * t.rec_rows * p.d);

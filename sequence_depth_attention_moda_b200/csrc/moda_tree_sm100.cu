@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             r.end_segment();
         }
     }
+    __syncwarp();        // a barrier counts a warp when the first of its lanes arrives
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
