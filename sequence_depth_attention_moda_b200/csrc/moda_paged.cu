@@ -412,6 +412,10 @@ moda_status launched(cudaError_t e, const char* what) {
     return api_fail(MODA_ERR_CUDA, msg);
 }
 
+moda_status too_many_tiles() {
+    return failf(MODA_ERR_UNSUPPORTED, "the block table's length times N passes 2^31 tiles");
+}
+
 moda_status no_device() { return api_fail(MODA_ERR_CUDA, "no usable CUDA device"); }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -427,6 +431,13 @@ moda_status guarded(F&& f) noexcept {
 }
 
 }  // namespace
+
+// The most tiles the schedule can meet: every request at the table's length,
+// every new token's depth rows in a tile of their own.
+static double most_tiles(const Paged& p, const TreePlan& t) {
+    const double groups = p.B + double(p.N) / t.Tg;
+    return p.Hk * (groups * (double(p.max_pages) * p.page / t.KT + 1) + double(p.N) * t.dsplit);
+}
 
 TreePlan tree_plan(const Paged& p) {
     TreePlan t;
@@ -560,7 +571,10 @@ size_t moda_tree_decode_workspace_size(const moda_paged_shape* shape) {
     guarded([&]() -> moda_status {
         Paged p{};
         const moda_status st = check_tree(shape, &p);
-        if (st == MODA_OK) bytes = p.B == 0 || p.N == 0 ? 0 : tree_plan(p).bytes;
+        if (st != MODA_OK) return st;
+        const TreePlan t = tree_plan(p);
+        if (p.B > 0 && p.N > 0 && most_tiles(p, t) > 2147483647.0) return too_many_tiles();
+        bytes = p.B == 0 || p.N == 0 ? 0 : t.bytes;
         return st;
     });
     return bytes;
@@ -587,6 +601,7 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         unsigned int* status = device_status_word();
         if (!status) return no_device();
         const TreePlan t = tree_plan(p);
+        if (most_tiles(p, t) > 2147483647.0) return too_many_tiles();
         if (ws_bytes < t.bytes)
             return failf(MODA_ERR_WORKSPACE, "moda_tree_decode needs %lld bytes of workspace (got %lld)",
                          static_cast<long long>(t.bytes), static_cast<long long>(ws_bytes));

@@ -31,10 +31,11 @@ namespace tree {
 
 // The job that holds a CTA's first tile, left for the combine kernel.
 struct CtaHeader {
-    long long x_total;     // tiles of the whole call
-    long long job_start;   // first tile of the job
+    int x_total;           // tiles of the whole call
+    int job_start;         // first tile of the job
     int nt;                // its tiles
     int b, hk, group;
+    int pad[2];
 };
 
 struct TreeArgs {
@@ -103,38 +104,40 @@ __device__ __forceinline__ void set_group(const TreeArgs& a, Job& j, int group) 
 }
 
 // Tiles of one KV head of a request.
-__device__ __forceinline__ long long head_tiles(const TreeArgs& a, const Request& r) {
+__device__ __forceinline__ int head_tiles(const TreeArgs& a, const Request& r) {
     Job j;
     j.r = r;
     const int ng = groups_of(a, r);
     if (ng == 0) return 0;
-    if (a.mask) {                       // all groups but the last are alike
-        set_group(a, j, ng - 1);
-        long long t = j.nt;
-        if (ng > 1) {
-            set_group(a, j, 0);
-            t += static_cast<long long>(j.nt) * (ng - 1);
-        }
-        return t;
-    }
-    long long t = 0;
-    for (int g = 0; g < ng; ++g) {
-        set_group(a, j, g);
-        t += j.nt;
+    set_group(a, j, ng - 1);
+    int t = j.nt;
+    if (ng > 1) {                       // all groups but the last are alike, but for a chain's keys
+        set_group(a, j, 0);
+        t += j.nt * (ng - 1);
+        if (!a.mask)
+            for (int g = 1; g < ng - 1; ++g) t += (r.held + (g + 1) * a.Tg + a.KT - 1) / a.KT - j.nseq;
     }
     return t;
 }
 
 // Where a CTA starts, in shared memory; written by schedule().
 struct Start {
-    long long warp_sum[32];
-    long long x_total;
+    int warp_sum[32];
     int b, hk, group, i0;    // first job and the first tile within it
     Request r;
     int count;               // tiles of this CTA
 };
 
-__device__ __forceinline__ long long range_begin(long long c, long long x, long long p) { return c * x / p; }
+// First tile of range c of P over x tiles.
+__device__ __forceinline__ int range_begin(int c, int x, int P) {
+    const int q = x / P, rem = x - q * P;
+    return c * q + min(c, rem);
+}
+// The range that holds tile t.
+__device__ __forceinline__ int range_of(int t, int x, int P) {
+    const int q = x / P, rem = x - q * P;
+    return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q;
+}
 
 // Called by all threads of the CTA: finds the CTA's range and writes its
 // header.  Ends with a __syncthreads.
@@ -143,68 +146,62 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
     const int lane = tid & 31, warp = tid >> 5;
     const int ch = (a.B + nth - 1) / nth;
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += head_tiles(a, load_request(a, b)) * a.Hk;
-    long long inc = mine;
-#pragma unroll
+    Request r = {};
+    int ht = 0, mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        r = load_request(a, b);
+        ht = head_tiles(a, r);
+        mine += ht * a.Hk;
+    }
+    int inc = mine;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
     }
     if (lane == 31) s->warp_sum[warp] = inc;
     if (tid == 0) s->count = 0;
     __syncthreads();
-    long long base = 0, total = 0;
+    int at = inc - mine, total = 0;
+#pragma unroll 1
     for (int w = 0; w < (nth >> 5); ++w) {
-        if (w < warp) base += s->warp_sum[w];
+        if (w < warp) at += s->warp_sum[w];
         total += s->warp_sum[w];
     }
-    const long long pre = base + inc - mine;
-    const long long P = min(static_cast<long long>(a.n_cta), total);
-    const long long c = blockIdx.x;
-    CtaHeader h;
-    h.x_total = total;
-    h.job_start = 0;
-    h.nt = h.b = h.hk = h.group = 0;
+    const int P = min(a.n_cta, total), c = static_cast<int>(blockIdx.x);
     if (c < P) {
-        const long long lo = range_begin(c, total, P), hi = range_begin(c + 1, total, P);
-        if (pre <= lo && lo < pre + mine) {
-            long long at = pre;
-            for (int b = b0; b < b1; ++b) {
-                Job j;
-                j.r = load_request(a, b);
-                const long long ht = head_tiles(a, j.r);
-                if (lo >= at + ht * a.Hk) {
+        const int lo = range_begin(c, total, P);
+        if (at <= lo && lo < at + mine) {
+            int b = b0;
+            if (ch > 1) {                // which of this thread's requests
+                for (;; ++b) {
+                    r = load_request(a, b);
+                    ht = head_tiles(a, r);
+                    if (lo < at + ht * a.Hk) break;
                     at += ht * a.Hk;
-                    continue;
                 }
-                const int hk = static_cast<int>((lo - at) / ht);
-                at += ht * hk;
-                int g = 0;
-                for (;; ++g) {
-                    set_group(a, j, g);
-                    if (lo < at + j.nt) break;
-                    at += j.nt;
-                }
-                s->b = b;
-                s->hk = hk;
-                s->group = g;
-                s->i0 = static_cast<int>(lo - at);
-                s->r = j.r;
-                s->count = static_cast<int>(hi - lo);
-                h.job_start = at;
-                h.nt = j.nt;
-                h.b = b;
-                h.hk = hk;
-                h.group = g;
-                a.hdr[c] = h;
-                break;
             }
+            const int hk = (lo - at) / ht;
+            at += ht * hk;
+            Job j;
+            j.r = r;
+            int g = 0;
+            for (;; ++g) {
+                set_group(a, j, g);
+                if (lo < at + j.nt) break;
+                at += j.nt;
+            }
+            s->b = b;
+            s->hk = hk;
+            s->group = g;
+            s->i0 = lo - at;
+            s->r = r;
+            s->count = range_begin(c + 1, total, P) - lo;
+            a.hdr[c] = CtaHeader{total, at, j.nt, b, hk, g, {0, 0}};
         }
     } else if (tid == 0) {
-        a.hdr[c] = h;
+        a.hdr[c] = CtaHeader{total, 0, 0, 0, 0, 0, {0, 0}};
     }
-    if (tid == 0) s->x_total = total;
     __syncthreads();
 }
 

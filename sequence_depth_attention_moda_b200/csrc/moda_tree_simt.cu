@@ -305,13 +305,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_wait();
     const CtaHeader h = a.hdr[c];
-    const long long P = min(static_cast<long long>(a.n_cta), h.x_total);
+    const int P = min(a.n_cta, h.x_total);
     if (c >= P) return;
-    const long long prev = range_begin(c - 1, h.x_total, P);
+    const int prev = range_begin(c - 1, h.x_total, P);
     if (h.job_start >= range_begin(c, h.x_total, P) || h.job_start < prev) return;
-    const long long end = h.job_start + h.nt;
     // records: range c-1 (slot 0 if the job is its first), then slot 0 of each range that begins inside the job
-    const int n = static_cast<int>((end * P - 1) / h.x_total) - c + 2;    // up to the range that holds tile end - 1
+    const int n = range_of(h.job_start + h.nt - 1, h.x_total, P) - c + 2;
     auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(c - 1 + i) + (i == 0 && h.job_start > prev); };
     Job j;
     j.b = h.b;

@@ -144,7 +144,7 @@ __device__ __forceinline__ int tile_rows(const TreeArgs& a, const Walk& w, int i
 
 // A lane's share of a tile's load: one box of a page, or of a token's depth rows.
 struct Box {
-    bool mine, dep;
+    bool mine, dep, once;
     int c1, c2, c3;      // coordinates (c0 is the slab)
     int row;             // first row in the tile
     uint32_t bytes;      // of the whole tile
@@ -152,6 +152,7 @@ struct Box {
 __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Walk& w, int i, int lane) {
     Box x;
     x.dep = i >= w.j.nseq;
+    x.once = w.j.r.n <= a.Tg;        // one group: no other job reads these keys
     x.mine = false;
     x.c1 = x.c2 = x.c3 = x.row = 0;
     if (!x.dep) {
@@ -281,6 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
     const uint32_t tmem = *tmem_holder;
     auto wait = [&](int bar, uint32_t phase) -> bool { return mbar_wait(&bars[bar], phase & 1, a.status, abort_flag); };
     auto wait_all = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
+    // Tiles that this call reads once leave L2 first: what else lives there (the
+    // kernel's own code, tables, records) then survives a cache of many GB.
+    const uint64_t once = policy_evict_first();
     // one box a lane: arms the stage's barrier for the whole tile, then loads
     auto load_tile = [&](const Box& x, int full, unsigned char* stage, const TmaMap* seq, const TmaMap* depth) {
         if (lane == 0) mbar_arrive_expect_tx(&bars[full], x.bytes);
@@ -289,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             unsigned char* dst = stage + x.row * 128;
 #pragma unroll
             for (int y = 0; y < L::kSlabs; ++y) {
-                if (x.dep) tma_load_4d(dst + y * kSlab, depth, &bars[full], y * 64, x.c1, x.c2, x.c3);
+                if (x.dep) tma_load_4d_hint(dst + y * kSlab, depth, &bars[full], y * 64, x.c1, x.c2, x.c3, once);
+                else if (x.once) tma_load_3d_hint(dst + y * kSlab, seq, &bars[full], y * 64, x.c1, x.c2, once);
                 else tma_load_3d(dst + y * kSlab, seq, &bars[full], y * 64, x.c1, x.c2);
             }
         }
