@@ -36,6 +36,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "moda_tree.cuh"
 
 namespace moda {
@@ -499,113 +501,119 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         bool ok = true;
         for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
             r.segment(a, w);
-            // per slot (selects, so that they stay in registers); l: this half's share
-            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // per slot; l: this half's share
             int prev0 = -1, prev1 = -1;               // the slot's last block in this segment
-            for (int i = w.i0; ok && i < w.i1; ++i) {
-                const bool dep = i >= w.j.nseq;
-                const bool masked = dep || (i + 1) * kTile > w.j.r.held;
-                const int dt = dep ? dep_index(w, i) : 0;
-#pragma unroll 1
-                for (int s = r.first; s <= r.last; ++s) {
-                    if (!r.takes(w, i, s)) continue;
-                    const int sb = r.b % L::kNS;
-                    if (!wait_all(L::kSFull + sb, r.b / L::kNS)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+            const int n_tok0 = sub_tokens(a, w.j, 0), n_tok1 = r.two ? sub_tokens(a, w.j, 1) : n_tok0;
+            // One block: slot s, tile i; `masks`: some key of the tile is hidden from some row.
+            auto block = [&](auto masks, int i, int s, int n_tok, float& m, float& l, int& prev) -> bool {
+                constexpr bool kMasks = decltype(masks)::value;
+                const int sb = r.b % L::kNS;
+                if (!wait_all(L::kSFull + sb, r.b / L::kNS)) return false;
+                tc_fence_after();
+                if (row0 < n_tok * a.G) {             // some row of the warp is real
                     const uint32_t s_addr = lane_base + sb * 128;
-                    float m = s ? m1 : m0, l = s ? l1 : l0;
-                    const int prev = s ? prev1 : prev0;
-                    const int n_tok = sub_tokens(a, w.j, r.sub(s));
                     const bool real = t_off < n_tok && t_off < a.Tq;
-                    if (row0 < n_tok * a.G) {         // some row of the warp is real
-                        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};   // of this thread's 64 columns
-                        if (masked && real) {
+                    uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;   // of this thread's 64 columns
+                    bool blind = false;               // none of the warp's tokens is in this depth tile
+                    if constexpr (kMasks) {
+                        const bool dep = i >= w.j.nseq;
+                        if (real) {
                             const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                vis[h] = dep ? dep_visible(a, t_off, dt, half * 64 + 32 * h)
-                                             : seq_visible(a, w.j.r, token, i * kTile + half * 64 + 32 * h);
+                            const int dt = dep_index(w, i);
+                            const int c = half * 64;
+                            vis0 = dep ? dep_visible(a, t_off, dt, c) : seq_visible(a, w.j.r, token, i * kTile + c);
+                            vis1 = dep ? dep_visible(a, t_off, dt, c + 32) : seq_visible(a, w.j.r, token, i * kTile + c + 32);
                         }
-                        uint32_t pk[32];
-                        if (dep && !__any_sync(0xffffffffu, real && (vis[0] | vis[1]))) {
-                            // none of the warp's tokens is in this tile
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) pk[e] = 0u;
-                        } else {
-                            uint32_t x[64];
-                            tmem_ld16x2_32<64>(s_addr, x);
-                            tmem_ld16x2_32<64>(s_addr + 32, x + 32);
-                            tmem_wait_ld();
-                            reg_fence<64>(x);
-                            if (masked) {
-#pragma unroll
-                                for (int e = 0; e < 64; ++e)
-                                    if (!(vis[e >> 5] >> (e & 31) & 1)) x[e] = __float_as_uint(-INFINITY);
-                            }
-                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int e = 0; e < 64; e += 8)
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    mx[u] = fmax3(mx[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
-                            float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16)) * sl2;
-                            // a new reference (a row's first: m = -inf)
-                            if (__any_sync(0xffffffffu, real && mn > m + kLazy)) {
-                                mn = fmaxf(m, mn);
-                                // o and l are 0 until a key is seen
-                                const float alpha = m == -INFINITY ? 1.0f : ex2(m - mn);
-                                l *= alpha;
-                                m = mn;
-                                if (prev >= 0) {
-                                    // O must hold the sum up to the slot's last block.  Blocks up to b - kNS are
-                                    // done (their buffer's reuse waited for them); a later one's barrier can
-                                    // not have moved on, since the next use of its buffer needs a later P.
-                                    if (prev > r.b - L::kNS &&
-                                        !wait_all(L::kSFree + prev % L::kNS, prev / L::kNS)) {
-                                        ok = false;
-                                        break;
-                                    }
-                                    tc_fence_after();
-#pragma unroll 1
-                                    for (int c = 0; c < D / 2; c += 32) {
-                                        uint32_t o[32];
-                                        const uint32_t at = lane_base + L::kColO + s * D + c;
-                                        tmem_ld16x2_32<D / 2>(at, o);
-                                        tmem_wait_ld();
-                                        reg_fence<32>(o);
-#pragma unroll
-                                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                        tmem_st16x2_32<D / 2>(at, o);
-                                    }
-                                    tmem_wait_st();
-                                }
-                            }
-                            // p = 2^(s sl2 - m), packed
-                            const float ref = m == -INFINITY ? 0.0f : m;     // a row that sees nothing yet: p = 0
-                            float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float p0 = ex2(fmaf(__uint_as_float(x[2 * e]), sl2, -ref));
-                                const float p1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), sl2, -ref));
-                                rs[e & 3] += p0 + p1;
-                                pk[e] = pack_bf16(p0, p1);
-                            }
-                            l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
-                        }
-                        __syncwarp();
-                        tmem_st16x2_32<32>(s_addr, pk);
-                        tmem_wait_st();
+                        blind = dep && !__any_sync(0xffffffffu, real && (vis0 | vis1));
                     }
-                    tc_fence_before();
+                    uint32_t pk[32];
+                    if (blind) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pk[e] = 0u;
+                    } else {
+                        uint32_t x[64];
+                        tmem_ld16x2_32<64>(s_addr, x);
+                        tmem_ld16x2_32<64>(s_addr + 32, x + 32);
+                        tmem_wait_ld();
+                        reg_fence<64>(x);
+                        if constexpr (kMasks) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                if (!((e < 32 ? vis0 : vis1) >> (e & 31) & 1)) x[e] = __float_as_uint(-INFINITY);
+                        }
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                mx[u] = fmax3(mx[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+                        // this half row's maximum: whether it passes the reference needs no
+                        // word from the other half (a row's first key: m = -inf)
+                        float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                        if (__any_sync(0xffffffffu, real && mn > m + kLazy)) {
+                            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
+                            mn = fmaxf(m, mn);
+                            // o and l are 0 until a key is seen
+                            const float alpha = m == -INFINITY ? 1.0f : ex2(m - mn);
+                            l *= alpha;
+                            m = mn;
+                            if (prev >= 0) {
+                                // O must hold the sum up to the slot's last block.  Blocks up to b - kNS are
+                                // done (their buffer's reuse waited for them); a later one's barrier can
+                                // not have moved on, since the next use of its buffer needs a later P.
+                                if (prev > r.b - L::kNS && !wait_all(L::kSFree + prev % L::kNS, prev / L::kNS)) return false;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D / 2; c += 32) {
+                                    uint32_t o[32];
+                                    const uint32_t at = lane_base + L::kColO + s * D + c;
+                                    tmem_ld16x2_32<D / 2>(at, o);
+                                    tmem_wait_ld();
+                                    reg_fence<32>(o);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tmem_st16x2_32<D / 2>(at, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        // p = 2^(s sl2 - m), packed
+                        const float ref = m == -INFINITY ? 0.0f : m;     // a row that sees nothing yet: p = 0
+                        float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float p0 = ex2(fmaf(__uint_as_float(x[2 * e]), sl2, -ref));
+                            const float p1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), sl2, -ref));
+                            rs[e & 3] += p0 + p1;
+                            pk[e] = pack_bf16(p0, p1);
+                        }
+                        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[L::kPReady + sb]);
-                    const int blk = r.b++;
-                    if (s) m1 = m, l1 = l, prev1 = blk;
-                    else m0 = m, l0 = l, prev0 = blk;
+                    tmem_st16x2_32<32>(s_addr, pk);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[L::kPReady + sb]);
+                prev = r.b++;
+                return true;
+            };
+            int i = w.i0;
+            const int open = min(w.i1, w.j.r.held / kTile);       // tiles of held keys alone
+            for (; ok && i < open; ++i) {
+                if (r.first == 0) ok = block(std::false_type{}, i, 0, n_tok0, m0, l0, prev0);
+                if (NQ == 2 && ok && r.last == 1) ok = block(std::false_type{}, i, 1, n_tok1, m1, l1, prev1);
+            }
+            for (; ok && i < w.i1; ++i) {
+#pragma unroll 1
+                for (int s = r.first; ok && s <= r.last; ++s) {
+                    if (!r.takes(w, i, s)) continue;
+                    float m = s ? m1 : m0, l = s ? l1 : l0;
+                    int prev = s ? prev1 : prev0;
+                    ok = block(std::true_type{}, i, s, s ? n_tok1 : n_tok0, m, l, prev);
+                    if (s) m1 = m, l1 = l, prev1 = prev;
+                    else m0 = m, l0 = l, prev0 = prev;
                 }
             }
             // ------------------------------------------------ end of segment --
