@@ -147,16 +147,16 @@ __device__ __forceinline__ int tile_rows(const TreeArgs& a, const Walk& w, int i
 // A lane's share of a tile's load: one box of a page, or of a token's depth rows.
 struct Box {
     bool mine, dep, once;
-    int c1, c2, c3;      // coordinates (c0 is the slab)
+    int c1, c2;          // coordinates (c0 is the slab)
     int row;             // first row in the tile
     uint32_t bytes;      // of the whole tile
 };
 __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Walk& w, int i, int lane) {
     Box x;
     x.dep = i >= w.j.nseq;
-    x.once = w.j.r.n <= a.Tg;        // one group: no other job reads these keys
+    x.once = x.dep || w.j.r.n <= a.Tg;   // one group: no other job reads these keys
     x.mine = false;
-    x.c1 = x.c2 = x.c3 = x.row = 0;
+    x.c1 = x.c2 = x.row = 0;
     if (!x.dep) {
         const int key = i * kTile + lane * box_rows;
         const int left = min(kTile, job_keys(a, w.j) - i * kTile);
@@ -172,19 +172,18 @@ __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int sla
     }
     const int sub = dep_sub(w, i), dt = dep_index(w, i);
     const int tok = w.j.r.cu0 + w.j.tok0 + sub * a.Tq;
-    x.c2 = w.j.hk;
     if (a.Lw <= kTile) {
         const int cnt = min(a.dtok, sub_tokens(a, w.j, sub) - dt * a.dtok);
         x.mine = lane < cnt;
         x.bytes = cnt * a.Lw * 128u * slabs;
         x.row = lane * a.Lp;
         x.c1 = a.win_lo;
-        x.c3 = tok + dt * a.dtok + lane;
+        x.c2 = (tok + dt * a.dtok + lane) * a.Hk + w.j.hk;
     } else {
         x.mine = lane == 0;
         x.bytes = kTile * 128u * slabs;                 // rows behind the last depth row read as zeros
         x.c1 = a.win_lo + dt % a.dsplit * kTile;
-        x.c3 = tok + dt / a.dsplit;
+        x.c2 = (tok + dt / a.dsplit) * a.Hk + w.j.hk;
     }
     return x;
 }
@@ -203,43 +202,56 @@ __device__ __forceinline__ bool clean_values(const TreeArgs& a, const Walk& w, i
 #pragma unroll 1
     for (int k = from / 32; k < groups; ++k) {           // 32 rows at a time: a row is 8 chunks of 16 bytes a slab
         const int mine = 32 * k + lane;
-        const bool real = mine < rows && !(dep && a.Lw <= kTile && mine % a.Lp >= a.Lw);
+        const bool real = mine < rows && !(dep && a.Lp != a.Lw && a.Lw <= kTile && mine % a.Lp >= a.Lw);
         const uint32_t there = __ballot_sync(0xffffffffu, real);
         const uint32_t masked = 32 * k >= from ? 0xffffffffu : 0xffffffffu << (from & 31);
-#pragma unroll 1
-        for (int x = 0; x < D / 64; ++x) {
-            uint4* p = reinterpret_cast<uint4*>(stage + x * kSlab) + 32 * 8 * k + lane;   // row 4u + lane/8, chunk lane%8
-            uint4 v[8];
+        uint4* p = reinterpret_cast<uint4*>(stage) + 32 * 8 * k + lane;   // row 4u + lane/8, chunk lane%8 of slab 0
+        uint32_t acc[4] = {0u, 0u, 0u, 0u};
+        if ((there & masked) == 0xffffffffu) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = p[32 * u];
-            uint32_t acc = 0u;
+            for (int x = 0; x < D / 64; ++x) {
+                uint4 v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int row = 4 * u + (lane >> 3);
-                if (!(there >> row & 1)) {
-                    p[32 * u] = make_uint4(0, 0, 0, 0);
-                } else if (masked >> row & 1) {
-                    acc = not_finite_acc(v[u].x, acc);
-                    acc = not_finite_acc(v[u].y, acc);
-                    acc = not_finite_acc(v[u].z, acc);
-                    acc = not_finite_acc(v[u].w, acc);
+                for (int u = 0; u < 8; ++u) v[u] = p[x * (kSlab / 16) + 32 * u];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    acc[0] = not_finite_acc(v[u].x, acc[0]);
+                    acc[1] = not_finite_acc(v[u].y, acc[1]);
+                    acc[2] = not_finite_acc(v[u].z, acc[2]);
+                    acc[3] = not_finite_acc(v[u].w, acc[3]);
                 }
             }
-            if (__any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0u)) {
-                bad = true;
+        } else {
 #pragma unroll 1
-                for (int u = 0; u < 8; ++u) {
-                    const int row = 4 * u + (lane >> 3);
-                    if (!(there & masked & (1u << row))) continue;
-                    uint4 y = p[32 * u];
-                    uint32_t* e = &y.x;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        if ((e[z] & 0x7f80u) == 0x7f80u) e[z] &= 0xffff0000u;
-                        if ((e[z] & 0x7f800000u) == 0x7f800000u) e[z] &= 0x0000ffffu;
-                    }
-                    p[32 * u] = y;
+            for (int y = 0; y < D / 8; ++y) {
+                const int row = 4 * (y & 7) + (lane >> 3);
+                uint4* q = p + (y >> 3) * (kSlab / 16) + 32 * (y & 7);
+                if (!(there >> row & 1)) {
+                    *q = make_uint4(0, 0, 0, 0);
+                } else if (masked >> row & 1) {
+                    const uint4 v = *q;
+                    acc[0] = not_finite_acc(v.x, acc[0]);
+                    acc[1] = not_finite_acc(v.y, acc[1]);
+                    acc[2] = not_finite_acc(v.z, acc[2]);
+                    acc[3] = not_finite_acc(v.w, acc[3]);
                 }
+            }
+        }
+        if (__any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0u)) {
+            bad = true;
+#pragma unroll 1
+            for (int y = 0; y < D / 8; ++y) {
+                const int row = 4 * (y & 7) + (lane >> 3);
+                if (!(there & masked & (1u << row))) continue;
+                uint4* q = p + (y >> 3) * (kSlab / 16) + 32 * (y & 7);
+                uint4 v = *q;
+                uint32_t* e = &v.x;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    if ((e[z] & 0x7f80u) == 0x7f80u) e[z] &= 0xffff0000u;
+                    if ((e[z] & 0x7f800000u) == 0x7f800000u) e[z] &= 0x0000ffffu;
+                }
+                *q = v;
             }
         }
     }
@@ -295,8 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             unsigned char* dst = stage + x.row * 128;
 #pragma unroll
             for (int y = 0; y < L::kSlabs; ++y) {
-                if (x.dep) tma_load_4d_hint(dst + y * kSlab, depth, &bars[full], y * 64, x.c1, x.c2, x.c3, once);
-                else if (x.once) tma_load_3d_hint(dst + y * kSlab, seq, &bars[full], y * 64, x.c1, x.c2, once);
+                if (x.once) tma_load_3d_hint(dst + y * kSlab, x.dep ? depth : seq, &bars[full], y * 64, x.c1, x.c2, once);
                 else tma_load_3d(dst + y * kSlab, seq, &bars[full], y * 64, x.c1, x.c2);
             }
         }
@@ -393,7 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             // bounded like every wait
             if (moved) {
                 t0 = 0;
-            } else if ((spins & 63u) == 0u) {
+                continue;
+            }
+            __nanosleep(32);             // two softmax warps share this warp's scheduler
+            if ((spins & 63u) == 0u) {
                 const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer(), 0);
                 if (t0 == 0) t0 = now;
                 const bool late = now - t0 > kWaitTimeoutNs;
@@ -696,12 +710,10 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
     if (p.Lw > 0) {
         // one token's depth rows a box, so that tokens start on 8-row boundaries
         // of the tile and no box reaches into tokens the job does not have
-        const uint64_t row = D * 2;
-        const uint64_t dims[4] = {D, static_cast<uint64_t>(p.L), static_cast<uint64_t>(p.Hk), static_cast<uint64_t>(p.N)};
-        const uint64_t strides[3] = {row, row * p.L, row * p.L * p.Hk};
-        const uint32_t box[4] = {64, static_cast<uint32_t>(p.Lw < kTile ? p.Lw : kTile), 1, 1};
-        if ((e = make_tma_4d_bf16(&g.tkd, a.kd, dims, strides, box)) != cudaSuccess) return e;
-        if ((e = make_tma_4d_bf16(&g.tvd, a.vd, dims, strides, box)) != cudaSuccess) return e;
+        const uint32_t rows = static_cast<uint32_t>(p.Lw < kTile ? p.Lw : kTile);
+        const uint64_t slots = static_cast<uint64_t>(p.N) * p.Hk;
+        if ((e = make_tma_3d_bf16(&g.tkd, a.kd, D, p.L, slots, rows, 1)) != cudaSuccess) return e;
+        if ((e = make_tma_3d_bf16(&g.tvd, a.vd, D, p.L, slots, rows, 1)) != cudaSuccess) return e;
     } else {
         g.tkd = g.tk;
         g.tvd = g.tv;
