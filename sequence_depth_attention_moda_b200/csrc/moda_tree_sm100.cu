@@ -16,9 +16,7 @@
 // turn, so a job's products start while the one before is written out.
 //
 // Warps: 0 TMA producer (Q, K; a lane a page or a token, so pages as small
-// as 8 rows cost one issue each); 1 TMA producer of V, which also clears the V
-// rows that are not there and the values that are not finite (below); 2 issues
-// S = Q K^T, up to the number of S buffers ahead; 3 issues O += P V; 4..11
+// as 8 rows cost one issue each); 1 TMA producer of V; 2 issues S = Q K^T, up to the number of S buffers ahead; 3 issues O += P V; 4..11
 // softmax, 16 rows a warp and two threads a row (columns [0,64) and [64,128)): O
 // and l are rescaled only when the maximum passes the reference by more than
 // 2^8 (exact: any reference gives the same quotient), P in bf16 over the score
@@ -27,11 +25,12 @@
 // TMEM columns: S buffers from 0 (two for d = 128, three for d = 64), then two
 // O accumulators of d.
 //
-// Warp 1: a tile that ends a request's keys leaves rows of the V stage unwritten
-// (pages behind the last key are not loaded) or with what the page held; P is
-// 0 there, but 0 * NaN is not, so it stores zeros.  In rows that only some of the
-// query rows see (new keys, depth rows) it replaces infinities and NaN and
-// marks the segment (add_not_finite).  Tiles of held keys pass untouched.
+// A tile that ends a request's keys leaves rows of the V stage unwritten (pages
+// behind the last key are not loaded) or with what the page held; P is 0 there,
+// but 0 * NaN is not, so the softmax warps store zeros (16 rows each), before P
+// of the tile's first block is announced.  In rows that only some of the query
+// rows see (new keys, depth rows) they replace infinities and NaN and mark the
+// segment (add_not_finite).  Tiles of held keys pass untouched.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -52,7 +51,8 @@ constexpr int kSoftmaxWarps = 8;
 constexpr uint32_t kSlab = 128 * 128;        // 128 rows x 64 bf16
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;                // log2 by which a maximum may pass the reference
-constexpr int kMarks = 8;                    // segments whose marks are told apart
+constexpr int kMarks = 2;                    // segments whose marks are told apart: a warp marks segment k+1
+                                             // only when all have begun to write out segment k
 
 // NQ: query tiles of a job, and O accumulators.
 template <int D, int NQ>
@@ -70,7 +70,7 @@ struct Lay {
     static constexpr uint32_t kBar = kV + kVS * kTileBytes;
     // barrier indexes; from kPReady on they take an arrival of each softmax warp
     static constexpr int kQFull = 0, kQFree = NQ, kKFull = 2 * NQ, kKEmpty = kKFull + kKS, kVFull = kKEmpty + kKS,
-                         kVFix = kVFull + kVS, kVEmpty = kVFix + kVS, kSFull = kVEmpty + kVS, kSFree = kSFull + kNS,
+                         kVEmpty = kVFull + kVS, kSFull = kVEmpty + kVS, kSFree = kSFull + kNS,
                          kOFull = kSFree + kNS, kPReady = kOFull + NQ, kOFree = kPReady + kNS, kNumBars = kOFree + NQ;
     static constexpr uint32_t kStart = kBar + (kNumBars * 8 + 15) / 16 * 16;
     static constexpr uint32_t kMisc = kStart + (sizeof(Start) + 15) / 16 * 16;  // tmem base, abort flag, marks
@@ -78,9 +78,6 @@ struct Lay {
     static constexpr uint32_t kDynSmem = kBytes + 1024;     // alignment slack
     static_assert(kColO + NQ * D <= kTmemCols, "TMEM columns");
     static_assert(kDynSmem <= 232448, "shared memory of one CTA");
-    // the softmax warps write out segment k before any P V of segment k+1 ends,
-    // so warp 1 is at most a V ring of tiles, each a segment, ahead of k
-    static_assert(kVS < kMarks, "marks of segments in flight must differ");
 };
 
 struct SmArgs {
@@ -188,75 +185,64 @@ __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int sla
     return x;
 }
 
-// Clears the rows of a V stage that P V covers (up to the next 16) but that
-// are not there, and takes infinities and NaN out of the rows that are masked
-// for some query row (whole warp).  True if it found any.
+// Rows r0 .. r0+15 of a V stage (whole warp): clears those that P V covers but
+// that are not there (from `rows` on; of every `pitch` rows those behind the
+// first `used`), and takes infinities and NaN out of those from row `from` on,
+// which are masked for some query row.  True if it found any.  A call of its
+// own, so that its registers are not the tile loop's.
 template <int D>
-__device__ __forceinline__ bool clean_values(const TreeArgs& a, const Walk& w, int i, unsigned char* stage, int lane) {
-    const bool dep = i >= w.j.nseq;
-    const int from = dep ? 0 : max(0, w.j.r.held - i * kTile);
-    if (from >= kTile) return false;
-    const int rows = tile_rows(a, w, i);
-    const int groups = (rows + 31) / 32;
-    bool bad = false;
-#pragma unroll 1
-    for (int k = from / 32; k < groups; ++k) {           // 32 rows at a time: a row is 8 chunks of 16 bytes a slab
-        const int mine = 32 * k + lane;
-        const bool real = mine < rows && !(dep && a.Lp != a.Lw && a.Lw <= kTile && mine % a.Lp >= a.Lw);
-        const uint32_t there = __ballot_sync(0xffffffffu, real);
-        const uint32_t masked = 32 * k >= from ? 0xffffffffu : 0xffffffffu << (from & 31);
-        uint4* p = reinterpret_cast<uint4*>(stage) + 32 * 8 * k + lane;   // row 4u + lane/8, chunk lane%8 of slab 0
-        uint32_t acc[4] = {0u, 0u, 0u, 0u};
-        if ((there & masked) == 0xffffffffu) {
+__device__ __noinline__ bool clean_values(unsigned char* stage, int r0, int rows, int from, int pitch, int used) {
+    const int lane = threadIdx.x & 31;
+    if (r0 >= rows || r0 + 16 <= from) return false;
+    const bool holes = pitch != used;
+    uint4* p = reinterpret_cast<uint4*>(stage) + r0 * 8 + lane;      // row r0 + 4u + lane/8, chunk lane%8 of a slab
+    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+    bool wrote = false;
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x) {
-                uint4 v[8];
+    for (int u = 0; u < 4; ++u) {
+        const int row = r0 + 4 * u + (lane >> 3);
+        const bool there = row < rows && !(holes && row % pitch >= used);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = p[x * (kSlab / 16) + 32 * u];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    acc[0] = not_finite_acc(v[u].x, acc[0]);
-                    acc[1] = not_finite_acc(v[u].y, acc[1]);
-                    acc[2] = not_finite_acc(v[u].z, acc[2]);
-                    acc[3] = not_finite_acc(v[u].w, acc[3]);
-                }
-            }
-        } else {
-#pragma unroll 1
-            for (int y = 0; y < D / 8; ++y) {
-                const int row = 4 * (y & 7) + (lane >> 3);
-                uint4* q = p + (y >> 3) * (kSlab / 16) + 32 * (y & 7);
-                if (!(there >> row & 1)) {
-                    *q = make_uint4(0, 0, 0, 0);
-                } else if (masked >> row & 1) {
-                    const uint4 v = *q;
-                    acc[0] = not_finite_acc(v.x, acc[0]);
-                    acc[1] = not_finite_acc(v.y, acc[1]);
-                    acc[2] = not_finite_acc(v.z, acc[2]);
-                    acc[3] = not_finite_acc(v.w, acc[3]);
-                }
-            }
-        }
-        if (__any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0u)) {
-            bad = true;
-#pragma unroll 1
-            for (int y = 0; y < D / 8; ++y) {
-                const int row = 4 * (y & 7) + (lane >> 3);
-                if (!(there & masked & (1u << row))) continue;
-                uint4* q = p + (y >> 3) * (kSlab / 16) + 32 * (y & 7);
-                uint4 v = *q;
-                uint32_t* e = &v.x;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    if ((e[z] & 0x7f80u) == 0x7f80u) e[z] &= 0xffff0000u;
-                    if ((e[z] & 0x7f800000u) == 0x7f800000u) e[z] &= 0x0000ffffu;
-                }
-                *q = v;
+        for (int x = 0; x < D / 64; ++x) {
+            uint4* q = p + x * (kSlab / 16) + 32 * u;
+            if (!there) {
+                *q = make_uint4(0, 0, 0, 0);
+                wrote = true;
+            } else if (row >= from) {
+                const uint4 v = *q;
+                acc[0] = not_finite_acc(v.x, acc[0]);
+                acc[1] = not_finite_acc(v.y, acc[1]);
+                acc[2] = not_finite_acc(v.z, acc[2]);
+                acc[3] = not_finite_acc(v.w, acc[3]);
             }
         }
     }
-    fence_proxy_async_smem();
+    const bool bad = __any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0u);
+    if (bad) {
+#pragma unroll 1
+        for (int y = 0; y < D / 16; ++y) {
+            const int row = r0 + 4 * (y & 3) + (lane >> 3);
+            if (row < from || row >= rows) continue;      // (a hole is zeros by now)
+            uint4* q = p + (y >> 2) * (kSlab / 16) + 32 * (y & 3);
+            uint4 v = *q;
+            uint32_t* e = &v.x;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                if ((e[z] & 0x7f80u) == 0x7f80u) e[z] &= 0xffff0000u;
+                if ((e[z] & 0x7f800000u) == 0x7f800000u) e[z] &= 0x0000ffffu;
+            }
+            *q = v;
+        }
+    }
+    if (__any_sync(0xffffffffu, wrote) || bad) fence_proxy_async_smem();
     return bad;
+}
+
+// Which of 64 columns a row sees: of a sequence tile (dt < 0) from key c on, or
+// of depth tile dt from row c on.  (A call, like clean_values.)
+__device__ __noinline__ uint2 tile_visible(const TreeArgs& a, const Request r, int token, int t_off, int dt, int c) {
+    if (dt >= 0) return make_uint2(dep_visible(a, t_off, dt, c), dep_visible(a, t_off, dt, c + 32));
+    return make_uint2(seq_visible(a, r, token, c), seq_visible(a, r, token, c + 32));
 }
 
 template <int D, int NQ>
@@ -322,9 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
 
     Walk w;
     Roles<NQ> r;
-    // 384 threads of 168 registers: 128 x 104 + 256 x 200
+    // 384 threads of 168 registers: 128 x 104 + 256 x 200, or 128 x 88 + 256 x 208
+    // (two query tiles' statistics); local memory has next to no L1 beside this
+    // much shared memory, so a spill in the block loop costs thousands of cycles
     if (warp < 4) {
-    regs_dec<104>();
+    regs_dec<NQ == 1 ? 104 : 88>();
     if (warp == 0) {
         // ------------------------------------------------- producer of Q, K --
         const uint32_t q_bytes = L::kSlabs * 128u * a.Tq * a.G;
@@ -361,64 +349,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             drain(L::kKFull, L::kKS, r.j);
         }
     } else if (warp == 1) {
-        // ---------------------------------- producer of V, rows not there ----
-        // Two walks over the tiles, the loads up to a ring ahead of the
-        // cleaning; whichever can go on does.
-        Walk wl;
-        int il = 0, jl = 0, ic = 0, jc = 0;
-        bool more_l = wl.begin(a, *start), more_c = w.begin(a, *start);
-        Box x;
-        if (more_l) {
-            il = wl.i0;
-            ic = w.i0;
-            x = tile_box(a, g.box_rows, L::kSlabs, wl, il, lane);
-        }
-        unsigned long long t0 = 0;
-        for (uint32_t spins = 0; more_c; ++spins) {
-            bool moved = false;
-            if (jc < jl && __all_sync(0xffffffffu, mbar_test(&bars[L::kVFull + jc % L::kVS], (jc / L::kVS) & 1))) {
-                const int st = jc % L::kVS;
-                const bool bad = clean_values<D>(a, w, ic, smem + L::kV + st * L::kTileBytes, lane);
-                if (bad && lane == 0) marks[w.seg % kMarks] = w.seg + 1;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::kVFix + st]);
-                ++jc;
-                if (++ic == w.i1) {
-                    more_c = w.next(a);
-                    ic = w.i0;
+        // ------------------------------------------------- producer of V -----
+        bool ok = true;
+        for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
+            for (int i = w.i0; i < w.i1; ++i, ++r.j) {
+                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, lane);
+                const int st = r.j % L::kVS;
+                if (r.j >= L::kVS && !wait_all(L::kVEmpty + st, r.j / L::kVS - 1)) {
+                    ok = false;
+                    break;
                 }
-                moved = true;
-            }
-            if (more_l && (jl < L::kVS || __all_sync(0xffffffffu, mbar_test(&bars[L::kVEmpty + jl % L::kVS],
-                                                                           (jl / L::kVS - 1) & 1)))) {
-                const int st = jl % L::kVS;
                 load_tile(x, L::kVFull + st, smem + L::kV + st * L::kTileBytes, &g.tv, &g.tvd);
-                ++jl;
-                if (++il == wl.i1) {
-                    more_l = wl.next(a);
-                    il = wl.i0;
-                }
-                if (more_l) x = tile_box(a, g.box_rows, L::kSlabs, wl, il, lane);
-                moved = true;
-            }
-            // bounded like every wait
-            if (moved) {
-                t0 = 0;
-                continue;
-            }
-            __nanosleep(32);             // two softmax warps share this warp's scheduler
-            if ((spins & 63u) == 0u) {
-                const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer(), 0);
-                if (t0 == 0) t0 = now;
-                const bool late = now - t0 > kWaitTimeoutNs;
-                if (late && lane == 0) {
-                    atomicOr(a.status, kStatusTimeout);
-                    *abort_flag = 1;
-                }
-                if (__any_sync(0xffffffffu, late || *abort_flag)) break;
             }
         }
-        if (lane == 0) drain(L::kVFull, L::kVS, jl);
+        if (lane == 0) drain(L::kVFull, L::kVS, r.j);
     } else if (warp == 2) {
         // ------------------------------------------------------ S = Q K^T -----
         if (elect_one()) {
@@ -471,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 for (int i = w.i0; ok && i < w.i1; ++i, ++r.j) {
                     const int st = r.j % L::kVS;
                     const int steps = (tile_rows(a, w, i) + 15) / 16;     // 16 keys each
-                    if (!(ok = wait(L::kVFix + st, r.j / L::kVS))) break;
+                    if (!(ok = wait(L::kVFull + st, r.j / L::kVS))) break;
                     for (int s = r.first; s <= r.last; ++s) {
                         if (!r.takes(w, i, s)) continue;
                         const int sb = r.b % L::kNS;
@@ -504,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
     }
     } else {
         // ------------------------------------------------------ softmax -------
-        regs_inc<200>();
+        regs_inc<NQ == 1 ? 200 : 208>();
         const int quarter = warp & 3;                 // TMEM lanes 32*quarter ..
         const int half = lane >> 4;                   // column half of the row
         const int row0 = quarter * 32 + ((warp - 4) >> 2) * 16;     // the warp's 16 rows
@@ -519,28 +463,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             int prev0 = -1, prev1 = -1;               // the slot's last block in this segment
             const int n_tok0 = sub_tokens(a, w.j, 0), n_tok1 = r.two ? sub_tokens(a, w.j, 1) : n_tok0;
             // One block: slot s, tile i; `masks`: some key of the tile is hidden from some row.
-            auto block = [&](auto masks, int i, int s, int n_tok, float& m, float& l, int& prev) -> bool {
+            // `clean`: the tile's values are looked over here (a tile's first block does).
+            auto block = [&](auto masks, int i, int s, int n_tok, float& m, float& l, int& prev, bool clean) -> bool {
                 constexpr bool kMasks = decltype(masks)::value;
                 const int sb = r.b % L::kNS;
                 if (!wait_all(L::kSFull + sb, r.b / L::kNS)) return false;
                 tc_fence_after();
-                if (row0 < n_tok * a.G) {             // some row of the warp is real
-                    const uint32_t s_addr = lane_base + sb * 128;
+                uint32_t pk[32];
+                const bool active = row0 < n_tok * a.G;    // some row of the warp is real
+                const uint32_t s_addr = lane_base + sb * 128;
+                if (active) {
                     const bool real = t_off < n_tok && t_off < a.Tq;
                     uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;   // of this thread's 64 columns
                     bool blind = false;               // none of the warp's tokens is in this depth tile
                     if constexpr (kMasks) {
                         const bool dep = i >= w.j.nseq;
                         if (real) {
-                            const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
-                            const int dt = dep_index(w, i);
-                            const int c = half * 64;
-                            vis0 = dep ? dep_visible(a, t_off, dt, c) : seq_visible(a, w.j.r, token, i * kTile + c);
-                            vis1 = dep ? dep_visible(a, t_off, dt, c + 32) : seq_visible(a, w.j.r, token, i * kTile + c + 32);
+                            const uint2 v = tile_visible(a, w.j.r, w.j.tok0 + r.sub(s) * a.Tq + t_off, t_off,
+                                                         dep ? dep_index(w, i) : -1, (dep ? 0 : i * kTile) + half * 64);
+                            vis0 = v.x;
+                            vis1 = v.y;
                         }
                         blind = dep && !__any_sync(0xffffffffu, real && (vis0 | vis1));
                     }
-                    uint32_t pk[32];
                     if (blind) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) pk[e] = 0u;
@@ -603,9 +548,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                         }
                         l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
                     }
+                }
+                if (active) {
                     __syncwarp();
                     tmem_st16x2_32<32>(s_addr, pk);
                     tmem_wait_st();
+                }
+                if constexpr (kMasks) {
+                    // S of this tile is done, so P V of tile j - kVS is, and the stage's phase is this tile's
+                    if (clean) {
+                        const int st = r.j % L::kVS;
+                        if (!wait_all(L::kVFull + st, r.j / L::kVS)) return false;
+                        const bool dep = i >= w.j.nseq;
+                        const bool bad = clean_values<D>(smem + L::kV + st * L::kTileBytes, (warp - 4) * 16,
+                                                         tile_rows(a, w, i), dep ? 0 : w.j.r.held - i * kTile,
+                                                         dep && a.Lw <= kTile ? a.Lp : kTile,
+                                                         dep && a.Lw <= kTile ? a.Lw : kTile);
+                        if (bad && lane == 0) marks[w.seg % kMarks] = w.seg + 1;
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -615,17 +575,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             };
             int i = w.i0;
             const int open = min(w.i1, w.j.r.held / kTile);       // tiles of held keys alone
-            for (; ok && i < open; ++i) {
-                if (r.first == 0) ok = block(std::false_type{}, i, 0, n_tok0, m0, l0, prev0);
-                if (NQ == 2 && ok && r.last == 1) ok = block(std::false_type{}, i, 1, n_tok1, m1, l1, prev1);
+            for (; ok && i < open; ++i, ++r.j) {
+                if (r.first == 0) ok = block(std::false_type{}, i, 0, n_tok0, m0, l0, prev0, false);
+                if (NQ == 2 && ok && r.last == 1) ok = block(std::false_type{}, i, 1, n_tok1, m1, l1, prev1, false);
             }
-            for (; ok && i < w.i1; ++i) {
+            for (; ok && i < w.i1; ++i, ++r.j) {
+                bool clean = true;
 #pragma unroll 1
                 for (int s = r.first; ok && s <= r.last; ++s) {
                     if (!r.takes(w, i, s)) continue;
                     float m = s ? m1 : m0, l = s ? l1 : l0;
                     int prev = s ? prev1 : prev0;
-                    ok = block(std::true_type{}, i, s, s ? n_tok1 : n_tok0, m, l, prev);
+                    ok = block(std::true_type{}, i, s, s ? n_tok1 : n_tok0, m, l, prev, clean);
+                    clean = false;
                     if (s) m1 = m, l1 = l, prev1 = prev;
                     else m0 = m, l0 = l, prev0 = prev;
                 }
