@@ -263,17 +263,22 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
     return (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
 
-// Which of the 32 sequence keys from key `k0` on the token sees: every held
-// key, and of the request's n new keys those whose bit its mask row has (in a
-// chain: those up to itself).
-__device__ __forceinline__ uint32_t seq_visible(const TreeArgs& a, const Request& r, int token, int k0) {
-    const int rel = k0 - r.held;
+// Which of the 32 new keys rel .. rel+31 (below 0: held keys) of a request's n a
+// token sees by its mask row: every held key, and those whose bit the row has.
+__device__ __forceinline__ uint32_t mask_visible(const uint32_t* row, int words, int n, int rel) {
     if (rel <= -32) return 0xffffffffu;
-    if (!a.mask) return bits_between(0, min(token + 1, r.n) - rel);
-    const uint32_t* row = a.mask + static_cast<size_t>(r.cu0 + token) * a.words;
     const int w = rel >> 5;             // floor
-    auto word = [&](int x) -> uint32_t { return x < 0 ? 0xffffffffu : (x < a.words ? __ldg(row + x) : 0u); };
-    return __funnelshift_r(word(w), word(w + 1), rel & 31) & bits_between(0, r.n - rel);
+    auto word = [&](int x) -> uint32_t { return x < 0 ? 0xffffffffu : (x < words ? __ldg(row + x) : 0u); };
+    return __funnelshift_r(word(w), word(w + 1), rel & 31) & bits_between(0, n - rel);
+}
+// The same without a mask (a chain): the new keys up to the token itself.
+__device__ __forceinline__ uint32_t chain_visible(int n, int token, int rel) {
+    return rel <= -32 ? 0xffffffffu : bits_between(0, min(token + 1, n) - rel);
+}
+// Which of the 32 sequence keys from key `k0` on the token sees.
+__device__ __forceinline__ uint32_t seq_visible(const TreeArgs& a, const Request& r, int token, int k0) {
+    return a.mask ? mask_visible(a.mask + static_cast<size_t>(r.cu0 + token) * a.words, a.words, r.n, k0 - r.held)
+                  : chain_visible(r.n, token, k0 - r.held);
 }
 
 // Which of 32 rows from row `c0` on of depth tile `dt` (of the row tile's

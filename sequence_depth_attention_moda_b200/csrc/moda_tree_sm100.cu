@@ -194,28 +194,40 @@ template <int D>
 __device__ __noinline__ bool clean_values(unsigned char* stage, int r0, int rows, int from, int pitch, int used) {
     const int lane = threadIdx.x & 31;
     if (r0 >= rows || r0 + 16 <= from) return false;
-    const bool holes = pitch != used;
     uint4* p = reinterpret_cast<uint4*>(stage) + r0 * 8 + lane;      // row r0 + 4u + lane/8, chunk lane%8 of a slab
+    uint4 v[4 * (D / 64)];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) v[u * (D / 64) + x] = p[x * (kSlab / 16) + 32 * u];
     uint32_t acc[4] = {0u, 0u, 0u, 0u};
-    bool wrote = false;
+    if (r0 >= from && r0 + 16 <= rows && pitch == used) {            // all there, all masked for somebody
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int row = r0 + 4 * u + (lane >> 3);
-        const bool there = row < rows && !(holes && row % pitch >= used);
+        for (int u = 0; u < 4 * (D / 64); ++u) {
+            acc[0] = not_finite_acc(v[u].x, acc[0]);
+            acc[1] = not_finite_acc(v[u].y, acc[1]);
+            acc[2] = not_finite_acc(v[u].z, acc[2]);
+            acc[3] = not_finite_acc(v[u].w, acc[3]);
+        }
+    } else {
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-            uint4* q = p + x * (kSlab / 16) + 32 * u;
-            if (!there) {
-                *q = make_uint4(0, 0, 0, 0);
-                wrote = true;
-            } else if (row >= from) {
-                const uint4 v = *q;
-                acc[0] = not_finite_acc(v.x, acc[0]);
-                acc[1] = not_finite_acc(v.y, acc[1]);
-                acc[2] = not_finite_acc(v.z, acc[2]);
-                acc[3] = not_finite_acc(v.w, acc[3]);
+        for (int u = 0; u < 4; ++u) {
+            const int row = r0 + 4 * u + (lane >> 3);
+            const bool there = row < rows && row % pitch < used;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const uint4 y = v[u * (D / 64) + x];
+                if (!there) {
+                    p[x * (kSlab / 16) + 32 * u] = make_uint4(0, 0, 0, 0);
+                } else if (row >= from) {
+                    acc[0] = not_finite_acc(y.x, acc[0]);
+                    acc[1] = not_finite_acc(y.y, acc[1]);
+                    acc[2] = not_finite_acc(y.z, acc[2]);
+                    acc[3] = not_finite_acc(y.w, acc[3]);
+                }
             }
         }
+        fence_proxy_async_smem();
     }
     const bool bad = __any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0u);
     if (bad) {
@@ -234,15 +246,14 @@ __device__ __noinline__ bool clean_values(unsigned char* stage, int r0, int rows
             *q = v;
         }
     }
-    if (__any_sync(0xffffffffu, wrote) || bad) fence_proxy_async_smem();
+    if (bad) fence_proxy_async_smem();
     return bad;
 }
 
-// Which of 64 columns a row sees: of a sequence tile (dt < 0) from key c on, or
-// of depth tile dt from row c on.  (A call, like clean_values.)
-__device__ __noinline__ uint2 tile_visible(const TreeArgs& a, const Request r, int token, int t_off, int dt, int c) {
-    if (dt >= 0) return make_uint2(dep_visible(a, t_off, dt, c), dep_visible(a, t_off, dt, c + 32));
-    return make_uint2(seq_visible(a, r, token, c), seq_visible(a, r, token, c + 32));
+// mask_visible of 64 keys.  (A call, like clean_values; its arguments are values,
+// since a reference to the kernel's parameters is read through global memory.)
+__device__ __noinline__ uint2 mask_visible64(const uint32_t* row, int words, int n, int rel) {
+    return make_uint2(mask_visible(row, words, n, rel), mask_visible(row, words, n, rel + 32));
 }
 
 template <int D, int NQ>
@@ -479,10 +490,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     if constexpr (kMasks) {
                         const bool dep = i >= w.j.nseq;
                         if (real) {
-                            const uint2 v = tile_visible(a, w.j.r, w.j.tok0 + r.sub(s) * a.Tq + t_off, t_off,
-                                                         dep ? dep_index(w, i) : -1, (dep ? 0 : i * kTile) + half * 64);
-                            vis0 = v.x;
-                            vis1 = v.y;
+                            const int c = half * 64;
+                            if (dep) {
+                                const int dt = dep_index(w, i);
+                                vis0 = dep_visible(a, t_off, dt, c);
+                                vis1 = dep_visible(a, t_off, dt, c + 32);
+                            } else {
+                                const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
+                                const int rel = i * kTile + c - w.j.r.held;
+                                if (a.mask) {
+                                    const uint2 v = mask_visible64(
+                                        a.mask + static_cast<size_t>(w.j.r.cu0 + token) * a.words, a.words, w.j.r.n, rel);
+                                    vis0 = v.x;
+                                    vis1 = v.y;
+                                } else {
+                                    vis0 = chain_visible(w.j.r.n, token, rel);
+                                    vis1 = chain_visible(w.j.r.n, token, rel + 32);
+                                }
+                            }
                         }
                         blind = dep && !__any_sync(0xffffffffu, real && (vis0 | vis1));
                     }
