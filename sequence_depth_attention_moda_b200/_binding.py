@@ -304,40 +304,60 @@ def moda_decode(shape: moda_shape, q, K, V, Kd, Vd, o, lse, ws, ws_bytes: int, s
            "moda_decode")
 
 
-def _paged_args(where: str, specs):
-    """Addresses of the arguments of a paged call, checked as `_expect` and
-    `_ptr` check the others; a spec is (name, tensor or int or None, least
-    element count, dtype).  Kept short: these calls run once a layer of every
-    decoding step, where the host's time counts."""
-    import torch
-    for name, x, count, dtype in specs:
-        if x is None or isinstance(x, int):
+# The paged calls run once a layer of every decoding step, next to kernels of a
+# few microseconds, so their marshalling is kept short: torch looked up once, a
+# tensor asked only for what the checks need, the stream taken as a number.
+_tp = None
+
+
+class _PagedTypes:
+    def __init__(self):
+        import torch
+        self.i32, self.i64, self.u8, self.f32 = torch.int32, torch.int64, torch.uint8, torch.float32
+        self.io = {MODA_BF16: torch.bfloat16, MODA_FP32: torch.float32}
+        # as numbers, straight from the binding torch.cuda itself uses
+        self.device = torch._C._cuda_getDevice if torch.cuda.is_available() else (lambda: -2)
+        self.raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else (lambda dev: 0)
+
+
+def _paged_types() -> "_PagedTypes":
+    global _tp
+    if _tp is None:
+        _tp = _PagedTypes()
+    return _tp
+
+
+def _paged_call(name: str, shape: moda_paged_shape, specs, tail, stream):
+    """Check the arguments as `_expect` and `_ptr` do for the other calls (a spec
+    is (name, tensor or int or None, least element count, dtype)) and call the
+    library on `stream` (None: torch's current one)."""
+    tp = _paged_types()
+    dev, args, bad = tp.device(), [], None
+    for arg, x, count, dtype in specs:
+        if x is None or x.__class__ is int:
+            args.append(x)
             continue
         if x.dtype is not dtype:
-            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} has dtype {x.dtype}, expected {dtype}")
+            raise MoDAError(MODA_ERR_INVALID_ARG, name, f"{arg} has dtype {x.dtype}, expected {dtype}")
         if x.numel() < count:
-            raise MoDAError(MODA_ERR_INVALID_ARG, where,
-                            f"{name} holds {x.numel()} elements, the shape needs {count}")
-    out, dev = [], None
-    for name, x, _, _ in specs:
-        if x is None or isinstance(x, int):
-            out.append(x)
-            continue
-        if not x.is_cuda:
-            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} is on {x.device}, not a CUDA device")
-        if not x.is_contiguous():
-            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} is not contiguous (row-major)")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if x.get_device() != dev:
-            raise MoDAError(MODA_ERR_INVALID_ARG, where, f"{name} is on {x.device}, current device is cuda:{dev}")
-        out.append(x.data_ptr())
-    return out
-
-
-def _paged_dtype(shape: moda_paged_shape):
-    import torch
-    return torch.float32 if shape.dtype == MODA_FP32 else torch.bfloat16
+            raise MoDAError(MODA_ERR_INVALID_ARG, name,
+                            f"{arg} holds {x.numel()} elements, the shape needs {count}")
+        if bad is None and (x.get_device() != dev or not x.is_contiguous()):
+            bad = arg, x
+        args.append(x.data_ptr())
+    if bad is not None:
+        arg, x = bad
+        what = (f"is on {x.device}, not a CUDA device" if not x.is_cuda else
+                "is not contiguous (row-major)" if x.get_device() == dev else
+                f"is on {x.device}, current device is cuda:{dev}")
+        raise MoDAError(MODA_ERR_INVALID_ARG, name, f"{arg} {what}")
+    if stream is None:
+        stream = tp.raw_stream(dev)
+    elif stream.__class__ is not int:
+        stream = stream.cuda_stream
+    rc = getattr(_lib or load(), name)(ctypes.byref(shape), *args, *tail, stream)
+    if rc != MODA_OK:
+        _check(rc, name)
 
 
 def moda_page_plan(shape: moda_paged_shape, held_len, want_len, block_table, free_pages, free_count, cu_new,
@@ -345,36 +365,32 @@ def moda_page_plan(shape: moda_paged_shape, held_len, want_len, block_table, fre
     """Make room for want_len tokens a request (or give pages back): updates
     block_table, free_pages and free_count, writes cu_new, granted_len and
     slot_map."""
-    import torch
-    B, i32 = max(0, shape.B), torch.int32
-    args = _paged_args("moda_page_plan", (
+    tp, B = _paged_types(), max(0, shape.B)
+    i32 = tp.i32
+    _paged_call("moda_page_plan", shape, (
         ("held_len", held_len, B, i32), ("want_len", want_len, B, i32),
         ("block_table", block_table, B * shape.max_pages, i32), ("free_pages", free_pages, shape.n_pages, i32),
         ("free_count", free_count, 1, i32), ("cu_new", cu_new, B + 1, i32), ("granted_len", granted_len, B, i32),
-        ("slot_map", slot_map, shape.N, torch.int64)))
-    _check(load().moda_page_plan(ctypes.byref(shape), *args, _stream(stream)), "moda_page_plan")
+        ("slot_map", slot_map, shape.N, tp.i64)), (), stream)
 
 
 def moda_cache_append(shape: moda_paged_shape, k_new, v_new, slot_map, k_cache, v_cache, stream=None):
     """Write the rows of k_new and v_new [N, Hk, d] into their cache slots."""
-    import torch
-    io = _paged_dtype(shape)
-    row, cache = shape.N * shape.Hk * shape.d, shape.n_pages * shape.Hk * shape.page_size * shape.d
-    args = _paged_args("moda_cache_append", (
-        ("k_new", k_new, row, io), ("v_new", v_new, row, io), ("slot_map", slot_map, shape.N, torch.int64),
-        ("k_cache", k_cache, cache, io), ("v_cache", v_cache, cache, io)))
-    _check(load().moda_cache_append(ctypes.byref(shape), *args, _stream(stream)), "moda_cache_append")
+    tp = _paged_types()
+    io, head = tp.io.get(shape.dtype), shape.Hk * shape.d
+    row, cache = shape.N * head, shape.n_pages * shape.page_size * head
+    _paged_call("moda_cache_append", shape, (
+        ("k_new", k_new, row, io), ("v_new", v_new, row, io), ("slot_map", slot_map, shape.N, tp.i64),
+        ("k_cache", k_cache, cache, io), ("v_cache", v_cache, cache, io)), (), stream)
 
 
 def moda_tree_mask(shape: moda_paged_shape, parent, cu_new, held_len, mask, position, stream=None):
     """Ancestor bits (int32 words) and positions of drafted trees; held_len
     may be None (positions from 0)."""
-    import torch
-    i32, B, N = torch.int32, max(0, shape.B), shape.N
-    args = _paged_args("moda_tree_mask", (
+    i32, B, N = _paged_types().i32, max(0, shape.B), shape.N
+    _paged_call("moda_tree_mask", shape, (
         ("parent", parent, N, i32), ("cu_new", cu_new, B + 1, i32), ("held_len", held_len, B, i32),
-        ("mask", mask, N * shape.mask_words, i32), ("position", position, N, i32)))
-    _check(load().moda_tree_mask(ctypes.byref(shape), *args, _stream(stream)), "moda_tree_mask")
+        ("mask", mask, N * shape.mask_words, i32), ("position", position, N, i32)), (), stream)
 
 
 def moda_tree_decode_workspace_size(shape: moda_paged_shape) -> int:
@@ -389,17 +405,16 @@ def moda_tree_decode(shape: moda_paged_shape, q, k_cache, v_cache, Kd, Vd, block
                      o, lse, ws, ws_bytes: int, stream=None):
     """Attention of the new tokens (a tree by its mask rows, or chains with
     mask None) over the paged cache and their own depth rows."""
-    import torch
-    io, i32 = _paged_dtype(shape), torch.int32
+    tp = _paged_types()
+    io, i32 = tp.io.get(shape.dtype), tp.i32
     B, N, Hk, d = max(0, shape.B), shape.N, shape.Hk, shape.d
-    row, dep, cache = N * shape.Hq * d, N * Hk * shape.L * d, shape.n_pages * Hk * shape.page_size * d
-    args = _paged_args("moda_tree_decode", (
+    row, dep, cache = N * shape.Hq * d, N * Hk * shape.L * d, shape.n_pages * shape.page_size * Hk * d
+    _paged_call("moda_tree_decode", shape, (
         ("q", q, row, io), ("k_cache", k_cache, cache, io), ("v_cache", v_cache, cache, io), ("Kd", Kd, dep, io),
         ("Vd", Vd, dep, io), ("block_table", block_table, B * shape.max_pages, i32),
         ("held_len", held_len, B, i32), ("cu_new", cu_new, B + 1, i32), ("mask", mask, N * shape.mask_words, i32),
-        ("o", o, row, io), ("lse", lse, N * shape.Hq, torch.float32), ("ws", ws, int(ws_bytes), torch.uint8)))
-    _check(load().moda_tree_decode(ctypes.byref(shape), *args, int(ws_bytes), _stream(stream)),
-           "moda_tree_decode")
+        ("o", o, row, io), ("lse", lse, N * shape.Hq, tp.f32), ("ws", ws, int(ws_bytes), tp.u8)),
+        (int(ws_bytes),), stream)
 
 
 def moda_selftest_wait_timeout(stream=None):

@@ -29,13 +29,19 @@
 namespace moda {
 namespace tree {
 
+// A request's clamped lengths.
+struct Request {
+    int held, n, cu0;
+};
+
 // The job that holds a CTA's first tile, left for the combine kernel.
 struct CtaHeader {
     int x_total;           // tiles of the whole call
     int job_start;         // first tile of the job
     int nt;                // its tiles
     int b, hk, group;
-    int pad[2];
+    Request r;
+    int pad[3];
 };
 
 struct TreeArgs {
@@ -58,11 +64,8 @@ struct TreeArgs {
     float scale_log2;
 };
 
-// A request's clamped lengths.  What lies outside the tables' bounds is cut
-// off, so that no index below leaves its array, and reported.
-struct Request {
-    int held, n, cu0;
-};
+// What lies outside the tables' bounds is cut off, so that no index below
+// leaves its array, and reported.
 __device__ __forceinline__ Request load_request(const TreeArgs& a, int b) {
     Request r;
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
@@ -197,10 +200,10 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
             s->i0 = lo - at;
             s->r = r;
             s->count = range_begin(c + 1, total, P) - lo;
-            a.hdr[c] = CtaHeader{total, at, j.nt, b, hk, g, {0, 0}};
+            a.hdr[c] = CtaHeader{total, at, j.nt, b, hk, g, r, {}};
         }
     } else if (tid == 0) {
-        a.hdr[c] = CtaHeader{total, 0, 0, 0, 0, 0, {0, 0}};
+        a.hdr[c] = CtaHeader{total, 0, 0, 0, 0, 0, {}, {}};
     }
     __syncthreads();
 }

@@ -297,12 +297,14 @@ cudaError_t launch_r(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
 // CTA (c, y) looks at the job that holds range c's first tile, and works if c
 // is the first range end inside that job; a warp takes one row.
 constexpr int kCombineWarps = 8;
+constexpr int kBatch = 8;
 
 template <typename E, int D>
 __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int C = D / 32;
     const int c = static_cast<int>(blockIdx.x) + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const CtaHeader h = a.hdr[c];
     const int P = min(a.n_cta, h.x_total);
@@ -315,30 +317,44 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     Job j;
     j.b = h.b;
     j.hk = h.hk;
-    j.r = load_request(a, h.b);
+    j.r = h.r;
     set_group(a, j, h.group);
     for (int row = blockIdx.y * kCombineWarps + warp; row < j.ntok * a.G; row += gridDim.y * kCombineWarps) {
-        float M = -INFINITY;
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, a.ml[slot_of(i) * a.rec_rows + row].x);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        const float ref = M == -INFINITY ? 0.0f : M;
-        float l = 0.0f, acc[C] = {};
+        // online over the records, kBatch of them in flight at a time
+        float M = -INFINITY, l = 0.0f, acc[C] = {};
         bool poison = false;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const size_t rec = slot_of(i) * a.rec_rows + row;
-            const float2 ml = a.ml[rec];
-            poison |= row_poisoned(ml.y);
-            const float wt = ex2(ml.x - ref);        // m = -inf: a record without keys, weight 0
-            float v[C];
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float2 ml[kBatch];
+            float v[kBatch][C];
 #pragma unroll
-            for (int e = 0; e < C; ++e) v[e] = a.po[rec * D + lane + 32 * e];
-            if (ml.x == -INFINITY && ml.y == 0.0f) continue;
-            l = fmaf(fabsf(ml.y), wt, l);
+            for (int u = 0; u < kBatch; ++u) {
+                ml[u] = make_float2(-INFINITY, 0.0f);
+                if (i0 + u >= n) continue;
+                const size_t rec = slot_of(i0 + u) * a.rec_rows + row;
+                ml[u] = a.ml[rec];
 #pragma unroll
-            for (int e = 0; e < C; ++e) acc[e] = fmaf(v[e], wt, acc[e]);
+                for (int e = 0; e < C; ++e) v[u][e] = a.po[rec * D + lane + 32 * e];
+            }
+            float mn = M;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, ml[u].x);
+            const float ref = mn == -INFINITY ? 0.0f : mn;
+            const float alpha = M == -INFINITY ? 1.0f : ex2(M - mn);     // l and acc are 0 until a key was seen
+            l *= alpha;
+#pragma unroll
+            for (int e = 0; e < C; ++e) acc[e] *= alpha;
+            M = mn;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                poison |= row_poisoned(ml[u].y);
+                if (ml[u].x == -INFINITY && ml[u].y == 0.0f) continue;    // a record without keys: no O was written
+                const float wt = ex2(ml[u].x - ref);
+                l = fmaf(fabsf(ml[u].y), wt, l);
+#pragma unroll
+                for (int e = 0; e < C; ++e) acc[e] = fmaf(v[u][e], wt, acc[e]);
+            }
         }
+        const float ref = M == -INFINITY ? 0.0f : M;
         const int tk = j.tok0 + row / a.G;
         const size_t orow = static_cast<size_t>(j.r.cu0 + tk) * a.Hq + j.hk * a.G + row % a.G;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;

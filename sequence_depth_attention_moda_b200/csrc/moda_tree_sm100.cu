@@ -287,6 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         prefetch_tmap(&g.tk);
         prefetch_tmap(&g.tv);
     }
+    // Launched while the grid before it ends: nothing of it is read, and nothing
+    // in memory written, before this.
+    griddep_wait();
     tc_fence_before();
     schedule(a, start);        // ends with a CTA barrier
     tc_fence_after();
@@ -707,8 +710,18 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
     }
     const void* f = reinterpret_cast<const void*>(tree_sm100_kernel<D, NQ>);
     if ((e = set_max_dynamic_smem(f, Lay<D, NQ>::kDynSmem)) != cudaSuccess) return e;
-    tree_sm100_kernel<D, NQ><<<t.n_cta, kThreads, Lay<D, NQ>::kDynSmem, s>>>(g);
-    return cudaGetLastError();
+    // set up (barriers, TMEM) while the grid before it in the stream ends
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(t.n_cta);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay<D, NQ>::kDynSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_sm100_kernel<D, NQ>, g);
 }
 
 }  // namespace
