@@ -25,18 +25,21 @@ namespace {
 // goes to place top-1-r of the free list and asked-for page q comes from place
 // top-1-q: a stack, the first request's pages on top, so that giving back what
 // a call took restores the list.  A request is served whole or not at all: if it
-// needs no page, or take_b + its own pages <= top.
+// needs no page, or take_b + its own pages <= top; those that are served pages
+// come before those that are refused some, so pages 0 .. granted-1 are theirs.
 //
-// Bound by latency, not by bytes: one launch of one cluster of 8 CTAs.  Every
-// CTA adds up all requests (8 KB for 1024 of them); the page moves and the
-// slots are dealt over the cluster's 128 warps, and the two hand-overs (released
-// pages written before any is taken, table entries written before slots read
-// them) are cluster barriers.
-constexpr int kPlanCtas = 8;
-constexpr int kPlanThreads = 512;
+// Bound by latency, not by bytes.  Every CTA adds up all requests (8 KB for 1024
+// of them) and keeps the prefixes in shared memory; then a thread finds its
+// page's or token's request by bisection, so few long requests spread over the
+// threads as many short ones do.  Released pages are written before any is
+// taken, and table entries before slots read them: CTA barriers where one CTA
+// does it all, else barriers of a cluster of 8 (see launch_plan for the choice).
+// The slots of many tokens are a grid of their own.
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kSlotChunk = 128;      // tokens a warp takes at a time
 constexpr int kMaxPlanRequests = 16384;
+constexpr int kSlotThreads = 256;
+constexpr int kSlotsPerLane = 4;
 
 struct PlanArgs {
     const int *held, *want;
@@ -44,37 +47,49 @@ struct PlanArgs {
     long long* slots;
     unsigned int* status;
     int B, N, page_shift, n_pages, max_pages;
+    int slots_here;                  // the plan kernel writes the slots itself
 };
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+template <int CTAS>
+__device__ __forceinline__ void plan_barrier() {
+    if (CTAS == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Exclusive prefix of `mine` over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ long long block_prefix(long long mine, long long* warp_sum, long long* total) {
+// Exclusive prefixes of x and y over the CTA's threads; tx and ty get the sums.
+__device__ __forceinline__ void block_prefix(long long& x, long long& y, longlong2* warp_sum, long long* tx,
+                                             long long* ty) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long inc = mine;
+    long long ix = x, iy = y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
+        const long long ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
+        if (lane >= o) {
+            ix += ux;
+            iy += uy;
+        }
     }
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = inc;
+    if (lane == 31) warp_sum[warp] = make_longlong2(ix, iy);
     __syncthreads();
-    long long base = 0, sum = 0;
+    long long wx = 0, wy = 0;            // lane w: the sum of warp w
+    if (lane < kPlanWarps) {
+        wx = warp_sum[lane].x;
+        wy = warp_sum[lane].y;
+    }
+    long long px = wx, py = wy;
 #pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w) {
-        if (w < warp) base += warp_sum[w];
-        sum += warp_sum[w];
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long ux = __shfl_up_sync(0xffffffffu, px, o), uy = __shfl_up_sync(0xffffffffu, py, o);
+        if (lane >= o) {
+            px += ux;
+            py += uy;
+        }
     }
-    *total = sum;
-    return base + inc - mine;
+    *tx = __shfl_sync(0xffffffffu, px, 31);
+    *ty = __shfl_sync(0xffffffffu, py, 31);
+    x = __shfl_sync(0xffffffffu, px - wx, warp) + ix - x;
+    y = __shfl_sync(0xffffffffu, py - wy, warp) + iy - y;
 }
 
 struct PlanRequest {
@@ -95,53 +110,94 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanArgs& a, int b) {
     return r;
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-page_plan_kernel(const __grid_constant__ PlanArgs a) {
-    extern __shared__ int plan_smem[];
-    __shared__ long long warp_sum[kPlanWarps];
-    int* s_cu = plan_smem;               // [B+1]
-    int* s_take = s_cu + a.B + 1;        // [B], -1: refused
-    int* s_drop = s_take + a.B;          // [B]
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int gwarp = static_cast<int>(cluster_rank()) * kPlanWarps + (tid >> 5);
-    const int n_warps = kPlanCtas * kPlanWarps;
-    const int ch = (a.B + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
-
-    // pages asked for (high half) and given back (low half)
-    long long mine = 0, total;
-    for (int b = b0; b < b1; ++b) {
-        const PlanRequest r = plan_request(a, b);
-        mine += (static_cast<long long>(max(r.need - r.have, 0)) << 32) + max(r.have - r.need, 0);
+// The last of n entries of an ascending list that is <= x (the first is 0).
+__device__ __forceinline__ int last_at_most(const int* list, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (list[mid] <= x) lo = mid;
+        else hi = mid - 1;
     }
-    long long at = block_prefix(mine, warp_sum, &total);
-    const int count0 = __ldcg(a.free_count);
-    const int count = min(max(count0, 0), a.n_pages);
-    const long long top = count + (total & 0xffffffffll);
-    if (count != count0 || top > a.n_pages) atomicOr(a.status, kStatusBadIndex);
-    // what is served: its tokens and pages
-    long long tokens = 0, pages = 0;
-    for (int b = b0; b < b1; ++b) {
-        const PlanRequest r = plan_request(a, b);
-        const int take = max(r.need - r.have, 0), drop = max(r.have - r.need, 0);
-        const int take0 = static_cast<int>(at >> 32), drop0 = static_cast<int>(at & 0xffffffffll);
-        at += (static_cast<long long>(take) << 32) + drop;
-        const bool served = r.fits && (take == 0 || static_cast<long long>(take0) + take <= top);
-        s_take[b] = served ? take0 : -1;
-        s_drop[b] = drop0;
-        if (served) {
-            tokens += max(r.want - r.held, 0);
-            pages += take;
+    return lo;
+}
+
+// Slots of tokens t0 + 32u + lane, u < kSlotsPerLane (whole warp); s_cu: cu in shared memory.
+__device__ __forceinline__ void write_slots(const PlanArgs& a, const int* s_cu, long long t0, int lane) {
+    const int n_in = min(s_cu[a.B], a.N);
+    long long slot[kSlotsPerLane];
+    int b = a.B > 0 && t0 < n_in ? last_at_most(s_cu, a.B, static_cast<int>(t0)) : 0;
+#pragma unroll
+    for (int u = 0; u < kSlotsPerLane; ++u) {
+        const long long t = t0 + 32 * u + lane;
+        slot[u] = -1;
+        if (t < n_in) {
+            while (s_cu[b + 1] <= t) ++b;
+            const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+            const int held = static_cast<int>(min(static_cast<long long>(max(__ldg(a.held + b), 0)), cap));
+            const int key = held + static_cast<int>(t - s_cu[b]);
+            const int page = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
+            if (page >= 0) slot[u] = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
         }
     }
-    long long n_pages_granted, n_tokens;
-    block_prefix(pages, warp_sum, &n_pages_granted);
-    long long c = block_prefix(tokens, warp_sum, &n_tokens);
+#pragma unroll
+    for (int u = 0; u < kSlotsPerLane; ++u) {
+        const long long t = t0 + 32 * u + lane;
+        if (t < a.N) a.slots[t] = slot[u];
+    }
+}
+
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    __shared__ longlong2 warp_sum[kPlanWarps];
+    int* s_cu = plan_smem;               // [B+1] prefixes of tokens,
+    int* s_take = s_cu + a.B + 1;        // [B]   of pages asked for,
+    int* s_drop = s_take + a.B;          // [B]   of pages given back
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int rank = CTAS == 1 ? 0 : static_cast<int>(blockIdx.x);     // one cluster
+    const int all = rank * kPlanThreads + tid;                          // thread of the grid
+    const int ch = (a.B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    const int count0 = __ldcg(a.free_count);
+    long long take = 0, drop = 0, takes, drops;
     for (int b = b0; b < b1; ++b) {
         const PlanRequest r = plan_request(a, b);
+        take += max(r.need - r.have, 0);
+        drop += max(r.have - r.need, 0);
+    }
+    block_prefix(take, drop, warp_sum, &takes, &drops);
+    const int count = min(max(count0, 0), a.n_pages);
+    const long long top = count + drops;
+    if (count != count0 || top > a.n_pages) atomicOr(a.status, kStatusBadIndex);
+    // what is served: its tokens and pages
+    long long tokens = 0, pages = 0, n_tokens, granted;
+    {
+        long long at = take, dr = drop;
+        for (int b = b0; b < b1; ++b) {
+            const PlanRequest r = plan_request(a, b);
+            const int t = max(r.need - r.have, 0);
+            s_take[b] = static_cast<int>(at);
+            s_drop[b] = static_cast<int>(dr);
+            at += t;
+            dr += max(r.have - r.need, 0);
+            if (r.fits && (t == 0 || at <= top)) {
+                tokens += max(r.want - r.held, 0);
+                pages += t;
+            }
+        }
+    }
+    block_prefix(tokens, pages, warp_sum, &n_tokens, &granted);
+    long long c = tokens, at = take;
+    for (int b = b0; b < b1; ++b) {
+        const PlanRequest r = plan_request(a, b);
+        const int t = max(r.need - r.have, 0);
+        at += t;
+        const bool served = r.fits && (t == 0 || at <= top);
         s_cu[b] = static_cast<int>(min(c, 0x7fffffffll));
-        const bool served = s_take[b] >= 0;
-        if (cluster_rank() == 0) {
+        if (rank == 0) {
             a.cu[b] = s_cu[b];
             a.granted[b] = served ? r.want : r.held;
         }
@@ -149,7 +205,7 @@ page_plan_kernel(const __grid_constant__ PlanArgs a) {
     }
     if (tid == 0) {
         s_cu[a.B] = static_cast<int>(min(n_tokens, 0x7fffffffll));
-        if (cluster_rank() == 0) {
+        if (rank == 0) {
             a.cu[a.B] = s_cu[a.B];
             if (n_tokens > a.N) atomicOr(a.status, kStatusBadIndex);
         }
@@ -157,57 +213,79 @@ page_plan_kernel(const __grid_constant__ PlanArgs a) {
     __syncthreads();
 
     // released pages onto the list
-    for (int b = gwarp; b < a.B; b += n_warps) {
-        const PlanRequest r = plan_request(a, b);
-        int* row = a.table + static_cast<size_t>(b) * a.max_pages;
-        for (int k = r.need + lane; k < r.have; k += 32) {
-            const long long place = top - 1 - (s_drop[b] + k - r.need);
-            const int page = __ldcg(row + k);
-            if (place < a.n_pages) a.free_pages[place] = page;
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) atomicOr(a.status, kStatusBadIndex);
-            row[k] = -1;
-        }
+    for (int x = all; x < static_cast<int>(drops); x += CTAS * kPlanThreads) {
+        const int b = last_at_most(s_drop, a.B, x);
+        int* entry = a.table + static_cast<size_t>(b) * a.max_pages + plan_request(a, b).need + (x - s_drop[b]);
+        const int page = __ldcg(entry);
+        const long long place = top - 1 - x;
+        if (place < a.n_pages) a.free_pages[place] = page;
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) atomicOr(a.status, kStatusBadIndex);
+        *entry = -1;
     }
-    cluster_barrier();
+    plan_barrier<CTAS>();
     // asked-for pages off it
-    for (int b = gwarp; b < a.B; b += n_warps) {
-        if (s_take[b] < 0) continue;
-        const PlanRequest r = plan_request(a, b);
-        int* row = a.table + static_cast<size_t>(b) * a.max_pages;
-        for (int k = r.have + lane; k < r.need; k += 32) {
-            const long long place = top - 1 - (s_take[b] + k - r.have);
-            row[k] = place < a.n_pages ? __ldcg(a.free_pages + place) : -1;
-        }
+    for (int x = all; x < static_cast<int>(granted); x += CTAS * kPlanThreads) {
+        const int b = last_at_most(s_take, a.B, x);
+        const long long place = top - 1 - x;
+        a.table[static_cast<size_t>(b) * a.max_pages + plan_request(a, b).have + (x - s_take[b])] =
+            place < a.n_pages ? __ldcg(a.free_pages + place) : -1;
     }
-    if (cluster_rank() == 0 && tid == 0)
-        *a.free_count = static_cast<int>(min(top - n_pages_granted, static_cast<long long>(a.n_pages)));
-    cluster_barrier();
-    // a slot a token
-    const int n_in = min(s_cu[a.B], a.N);
-    const long long chunks = (static_cast<long long>(a.N) + kSlotChunk - 1) / kSlotChunk;
-    for (long long ck = gwarp; ck < chunks; ck += n_warps) {
-        const long long t0 = ck * kSlotChunk;
-        int lo = 0, hi = a.B - 1;            // the last request that starts at or before t0
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_cu[mid] <= t0) lo = mid;
-            else hi = mid - 1;
-        }
-        int b = lo;
-#pragma unroll
-        for (int u = 0; u < kSlotChunk / 32; ++u) {
-            const long long t = t0 + 32 * u + lane;
-            if (t >= a.N) break;
-            long long slot = -1;
-            if (t < n_in) {
-                while (s_cu[b + 1] <= t) ++b;
-                const int key = plan_request(a, b).held + static_cast<int>(t - s_cu[b]);
-                const int page = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
-                if (page >= 0) slot = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-            }
-            a.slots[t] = slot;
-        }
-    }
+    if (rank == 0 && tid == 0) *a.free_count = static_cast<int>(min(top - granted, static_cast<long long>(a.n_pages)));
+    if (!a.slots_here) return;
+    plan_barrier<CTAS>();
+    for (long long t0 = (all >> 5) * 32ll * kSlotsPerLane; t0 < a.N; t0 += CTAS * kPlanThreads * kSlotsPerLane)
+        write_slots(a, s_cu, t0, lane);
+}
+
+// The slots of many tokens, after the plan.
+__global__ void __launch_bounds__(kSlotThreads) plan_slots_kernel(const __grid_constant__ PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    for (int b = threadIdx.x; b <= a.B; b += kSlotThreads) plan_smem[b] = __ldcg(a.cu + b);
+    __syncthreads();
+    const int per = kSlotThreads * kSlotsPerLane;
+    for (long long t0 = static_cast<long long>(blockIdx.x) * per + (threadIdx.x >> 5) * 32 * kSlotsPerLane; t0 < a.N;
+         t0 += static_cast<long long>(gridDim.x) * per)
+        write_slots(a, plan_smem, t0, threadIdx.x & 31);
+}
+
+// A launch that may be set up while the grid before it in the stream ends (the
+// kernels wait for it themselves).
+template <typename A>
+cudaError_t launch_dependent(void (*kernel)(A), unsigned grid, unsigned block, int smem, int cluster, cudaStream_t s,
+                             const A& a) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+cudaError_t launch_plan(PlanArgs& a, cudaStream_t s) {
+    // One CTA while its 1024 threads need few turns, else a cluster of 8; slots of
+    // their own from where 148 SMs gain more than the second launch costs.
+    const bool small = a.B <= kPlanThreads && a.N <= 2 * kPlanThreads * kSlotsPerLane;
+    a.slots_here = a.N <= 4 * kPlanThreads * kSlotsPerLane;
+    const int list = (a.B + 1) * static_cast<int>(sizeof(int)), smem = 3 * list;
+    const int most = 3 * (kMaxPlanRequests + 1) * static_cast<int>(sizeof(int));
+    auto kernel = small ? page_plan_kernel<1> : page_plan_kernel<8>;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), most);
+    if (e == cudaSuccess) e = launch_dependent(kernel, small ? 1 : 8, kPlanThreads, smem, small ? 1 : 8, s, a);
+    if (e != cudaSuccess || a.slots_here || a.N == 0) return e;
+    e = set_max_dynamic_smem(reinterpret_cast<const void*>(plan_slots_kernel), most / 3);
+    if (e != cudaSuccess) return e;
+    const long long per = kSlotThreads * kSlotsPerLane, want = (a.N + per - 1) / per, cap = 8ll * device_sm_count();
+    return launch_dependent(plan_slots_kernel, static_cast<unsigned>(want < cap ? want : cap), kSlotThreads, list, 1, s, a);
 }
 
 // ---------------------------------------------------------------- append ----
@@ -228,6 +306,8 @@ struct AppendArgs {
 
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     const long long first = static_cast<long long>(blockIdx.x) * (kAppendThreads * kAppendUnroll);
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const long long tok0 = first / a.row_chunks;
     const unsigned c0 = static_cast<unsigned>(first - tok0 * a.row_chunks);
     uint4 kv[kAppendUnroll], vv[kAppendUnroll];
@@ -282,6 +362,8 @@ struct MaskArgs {
 __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const __grid_constant__ MaskArgs a) {
     __shared__ int up[32 * kMaxMaskWords];
     const int b = blockIdx.x;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
     const int h = a.held ? __ldg(a.held + b) : 0;
     const int first = min(max(c0, 0), a.N);
@@ -500,13 +582,7 @@ moda_status moda_page_plan(const moda_paged_shape* shape, const int* held_len, c
         a.status = device_status_word();
         if (!a.status) return no_device();
         a.B = p.B; a.N = p.N; a.page_shift = p.page_shift; a.n_pages = p.n_pages; a.max_pages = p.max_pages;
-        const int smem = (3 * p.B + 1) * static_cast<int>(sizeof(int));
-        cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(page_plan_kernel),
-                                             (3 * kMaxPlanRequests + 1) * static_cast<int>(sizeof(int)));
-        if (e == cudaSuccess) {
-            page_plan_kernel<<<kPlanCtas, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-            e = cudaGetLastError();
-        }
+        const cudaError_t e = launch_plan(a, reinterpret_cast<cudaStream_t>(stream));
         return launched(e, "page plan launch");
     });
 }
@@ -539,9 +615,9 @@ moda_status moda_cache_append(const moda_paged_shape* shape, const void* k_new, 
         const long long per = kAppendThreads * kAppendUnroll;
         const long long grid = (a.n_chunks + per - 1) / per;
         if (grid > 0x7fffffffll) return failf(MODA_ERR_UNSUPPORTED, "N=%lld tokens are too many for one call", p.N);
-        cache_append_kernel<<<static_cast<unsigned>(grid), kAppendThreads, 0,
-                              reinterpret_cast<cudaStream_t>(stream)>>>(a);
-        return launched(cudaGetLastError(), "cache append launch");
+        return launched(launch_dependent(cache_append_kernel, static_cast<unsigned>(grid), kAppendThreads, 0, 1,
+                                         reinterpret_cast<cudaStream_t>(stream), a),
+                        "cache append launch");
     });
 }
 
@@ -561,8 +637,9 @@ moda_status moda_tree_mask(const moda_paged_shape* shape, const int* parent, con
         a.status = device_status_word();
         if (!a.status) return no_device();
         a.B = p.B; a.N = p.N; a.words = p.words;
-        tree_mask_kernel<<<p.B, kMaskThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-        return launched(cudaGetLastError(), "tree mask launch");
+        return launched(launch_dependent(tree_mask_kernel, static_cast<unsigned>(p.B), kMaskThreads, 0, 1,
+                                         reinterpret_cast<cudaStream_t>(stream), a),
+                        "tree mask launch");
     });
 }
 
