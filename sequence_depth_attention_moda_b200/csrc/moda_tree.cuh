@@ -64,22 +64,29 @@ struct TreeArgs {
     float scale_log2;
 };
 
-// What lies outside the tables' bounds is cut off, so that no index below
-// leaves its array, and reported.
-__device__ __forceinline__ Request load_request(const TreeArgs& a, int b) {
+// A request's lengths as the caller has them, and clamped: what lies outside
+// the tables' bounds is cut off, so that no index below leaves its array, and
+// reported.
+struct RawRequest {
+    int held, c0, c1;
+};
+__device__ __forceinline__ RawRequest load_raw(const TreeArgs& a, int b) {
+    return RawRequest{__ldg(a.held + b), __ldg(a.cu + b), __ldg(a.cu + b + 1)};
+}
+__device__ __forceinline__ Request clamp_request(const TreeArgs& a, const RawRequest& x) {
     Request r;
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
-    const int h = __ldg(a.held + b), c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-    r.held = static_cast<int>(min(static_cast<long long>(max(h, 0)), cap));
-    r.cu0 = min(max(c0, 0), a.N);
-    long long n = static_cast<long long>(c1) - c0;
+    r.held = static_cast<int>(min(static_cast<long long>(max(x.held, 0)), cap));
+    r.cu0 = min(max(x.c0, 0), a.N);
+    long long n = static_cast<long long>(x.c1) - x.c0;
     n = min(n, static_cast<long long>(a.N - r.cu0));
     n = min(n, cap - r.held);
     if (a.mask) n = min(n, 32ll * a.words);
     r.n = static_cast<int>(max(n, 0ll));
-    if (r.held != h || r.cu0 != c0 || r.n != c1 - c0) atomicOr(a.status, kStatusBadIndex);
+    if (r.held != x.held || r.cu0 != x.c0 || r.n != x.c1 - x.c0) atomicOr(a.status, kStatusBadIndex);
     return r;
 }
+__device__ __forceinline__ Request load_request(const TreeArgs& a, int b) { return clamp_request(a, load_raw(a, b)); }
 
 __device__ __forceinline__ int dep_tiles_of(const TreeArgs& a, int tokens) {
     if (a.Lw == 0 || tokens <= 0) return 0;
@@ -208,12 +215,14 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
     __syncthreads();
 }
 
-// Walks a CTA's jobs.
+// Walks a CTA's jobs.  The next request's lengths are asked for when a request
+// begins: under load such a read takes as long as a tile or two.
 struct Walk {
     Job j;
-    int i0, i1;      // this CTA's tiles of the job
-    int left;        // tiles left behind them
-    int seg;         // 0 for the first
+    RawRequest ahead;    // of request j.b + 1
+    int i0, i1;          // this CTA's tiles of the job
+    int left;            // tiles left behind them
+    int seg;             // 0 for the first
     __device__ __forceinline__ bool begin(const TreeArgs& a, const Start& s) {
         seg = 0;
         left = s.count;
@@ -221,6 +230,7 @@ struct Walk {
         j.b = s.b;
         j.hk = s.hk;
         j.r = s.r;
+        look_ahead(a);
         set_group(a, j, s.group);
         take(s.i0);
         return true;
@@ -234,7 +244,8 @@ struct Walk {
                 j.hk = 0;
                 do {
                     if (++j.b >= a.B) return false;
-                    j.r = load_request(a, j.b);
+                    j.r = clamp_request(a, ahead);
+                    look_ahead(a);
                 } while (j.r.n == 0);
             }
         }
@@ -250,6 +261,9 @@ struct Walk {
     }
 
    private:
+    __device__ __forceinline__ void look_ahead(const TreeArgs& a) {
+        if (j.b + 1 < a.B) ahead = load_raw(a, j.b + 1);
+    }
     __device__ __forceinline__ void take(int first) {
         i0 = first;
         i1 = min(j.nt, first + left);
@@ -295,13 +309,19 @@ __device__ __forceinline__ uint32_t dep_visible(const TreeArgs& a, int t, int dt
     return tok == t ? bits_between(0, a.Lw - (dt - tok * a.dsplit) * a.KT - c0) : 0u;
 }
 
-// The page of a request that holds key `key`; -1 (and a status) for an entry
-// that names no page of the cache.
-__device__ __forceinline__ int page_of(const TreeArgs& a, int b, int key) {
-    const int p = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
+// The block table's entry for a request's key `key`; the page an entry names, -1
+// (and a status) if it names none of the cache.
+__device__ __forceinline__ int table_entry(const TreeArgs& a, int b, int key) {
+    return __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
+}
+__device__ __forceinline__ int checked_page(const TreeArgs& a, int p) {
     if (static_cast<unsigned>(p) < static_cast<unsigned>(a.n_pages)) return p;
     atomicOr(a.status, kStatusBadIndex);
     return -1;
+}
+
+__device__ __forceinline__ int page_of(const TreeArgs& a, int b, int key) {
+    return checked_page(a, table_entry(a, b, key));
 }
 
 // ------------------------------------------------- values that are not finite --

@@ -58,6 +58,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
     Start* st = reinterpret_cast<Start*>(smem + L::kStart);
     int* spoison = reinterpret_cast<int*>(st + 1);
 
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     schedule(a, st);
     const int tid = threadIdx.x;
     const int ds = tid % DS;
@@ -289,8 +291,17 @@ cudaError_t launch_r(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
     const void* f = reinterpret_cast<const void*>(tree_simt_kernel<D, R>);
     const cudaError_t e = set_max_dynamic_smem(f, Lay<D, R>::kBytes);
     if (e != cudaSuccess) return e;
-    tree_simt_kernel<D, R><<<t.n_cta, kThreads, Lay<D, R>::kBytes, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(t.n_cta);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay<D, R>::kBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_simt_kernel<D, R>, a);
 }
 
 // Merges the records of a job that range ends cut: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).

@@ -148,7 +148,13 @@ struct Box {
     int row;             // first row in the tile
     uint32_t bytes;      // of the whole tile
 };
-__device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Walk& w, int i, int lane) {
+// Table entry for this lane's box of tile i (0 where it has none).
+__device__ __forceinline__ int box_entry(const TreeArgs& a, int box_rows, const Walk& w, int i, int lane) {
+    if (i >= min(w.i1, w.j.nseq) || lane * box_rows >= min(kTile, job_keys(a, w.j) - i * kTile)) return 0;
+    return table_entry(a, w.j.b, i * kTile + lane * box_rows);
+}
+__device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Walk& w, int i, int entry,
+                                        int lane) {
     Box x;
     x.dep = i >= w.j.nseq;
     x.once = x.dep || w.j.r.n <= a.Tg;   // one group: no other job reads these keys
@@ -160,7 +166,7 @@ __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int sla
         x.mine = lane * box_rows < left;
         x.bytes = ((left + box_rows - 1) / box_rows) * box_rows * 128u * slabs;
         if (x.mine) {
-            const int p = page_of(a, w.j.b, key);
+            const int p = checked_page(a, entry);
             x.row = lane * box_rows;
             x.c1 = key & ((1 << a.page_shift) - 1);
             x.c2 = p < 0 ? -1 : p * a.Hk + w.j.hk;      // outside: the box reads as zeros
@@ -346,8 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 }
             }
             if (!ok) break;
+            // table entries two tiles ahead: under load a read takes as long as a tile
+            int e0 = box_entry(a, g.box_rows, w, w.i0, lane), e1 = box_entry(a, g.box_rows, w, w.i0 + 1, lane);
             for (int i = w.i0; i < w.i1; ++i, ++r.j) {
-                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, lane);
+                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, e0, lane);
+                e0 = e1;
+                e1 = box_entry(a, g.box_rows, w, i + 2, lane);
                 const int st = r.j % L::kKS;
                 if (r.j >= L::kKS && !wait_all(L::kKEmpty + st, r.j / L::kKS - 1)) {
                     ok = false;
@@ -366,8 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         // ------------------------------------------------- producer of V -----
         bool ok = true;
         for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
+            int e0 = box_entry(a, g.box_rows, w, w.i0, lane), e1 = box_entry(a, g.box_rows, w, w.i0 + 1, lane);
             for (int i = w.i0; i < w.i1; ++i, ++r.j) {
-                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, lane);
+                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, e0, lane);
+                e0 = e1;
+                e1 = box_entry(a, g.box_rows, w, i + 2, lane);
                 const int st = r.j % L::kVS;
                 if (r.j >= L::kVS && !wait_all(L::kVEmpty + st, r.j / L::kVS - 1)) {
                     ok = false;
