@@ -514,11 +514,11 @@ moda_status guarded(F&& f) noexcept {
 
 }  // namespace
 
-// The most tiles the schedule can meet: every request at the table's length,
-// every new token's depth rows in a tile of their own.
-static double most_tiles(const Paged& p, const TreePlan& t) {
+// The most the schedule's costs can add up to: every request at the table's
+// length, every new token's depth rows in a tile of their own.
+static double most_cost(const Paged& p, const TreePlan& t) {
     const double groups = p.B + double(p.N) / t.Tg;
-    return p.Hk * (groups * (double(p.max_pages) * p.page / t.KT + 1) + double(p.N) * t.dsplit);
+    return p.Hk * (groups * (double(p.max_pages) * p.page / t.KT + 1) * t.tiles + double(p.N) * t.dsplit);
 }
 
 TreePlan tree_plan(const Paged& p) {
@@ -650,7 +650,7 @@ size_t moda_tree_decode_workspace_size(const moda_paged_shape* shape) {
         const moda_status st = check_tree(shape, &p);
         if (st != MODA_OK) return st;
         const TreePlan t = tree_plan(p);
-        if (p.B > 0 && p.N > 0 && most_tiles(p, t) > 2147483647.0) return too_many_tiles();
+        if (p.B > 0 && p.N > 0 && most_cost(p, t) > 2147483647.0) return too_many_tiles();
         bytes = p.B == 0 || p.N == 0 ? 0 : t.bytes;
         return st;
     });
@@ -678,7 +678,7 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         unsigned int* status = device_status_word();
         if (!status) return no_device();
         const TreePlan t = tree_plan(p);
-        if (most_tiles(p, t) > 2147483647.0) return too_many_tiles();
+        if (most_cost(p, t) > 2147483647.0) return too_many_tiles();
         if (ws_bytes < t.bytes)
             return failf(MODA_ERR_WORKSPACE, "moda_tree_decode needs %lld bytes of workspace (got %lld)",
                          static_cast<long long>(t.bytes), static_cast<long long>(ws_bytes));
@@ -695,6 +695,8 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         a.B = p.B; a.N = p.N; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.G; a.L = p.L; a.Lw = p.Lw; a.win_lo = p.win_lo;
         a.page_shift = p.page_shift; a.n_pages = p.n_pages; a.max_pages = p.max_pages; a.words = p.words;
         a.Tq = t.Tq; a.Tg = t.Tg; a.KT = t.KT; a.Lp = t.Lp; a.dtok = t.dtok; a.dsplit = t.dsplit;
+        a.cost1 = 1;
+        a.cost2 = t.tiles;
         a.rec_rows = t.rec_rows; a.n_cta = t.n_cta; a.scale_log2 = p.scale_log2;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         phase_mark(0, s);

@@ -8,8 +8,11 @@
 // reads tiles of KT key rows: first its sequence tiles (keys 0 .. held+n-1 of
 // the request, through the block table), then the depth tiles of its tokens.
 // Only the keys from `held` on and the depth rows are masked.  The jobs' tiles
-// form one list, in the order request, KV head, group, tile; CTA c of P owns
-// the contiguous range [c*X/P, (c+1)*X/P) of its X tiles.  Lengths live on the
+// form one list, in the order request, KV head, group, tile; each has a cost (a
+// sequence tile that two row tiles take costs more than one that a single one
+// takes), and CTA c of P owns the tiles that begin in the c-th of P equal parts
+// of the total cost X (X < 2^31, which the host checks, so 32 bits and no long
+// division; X / P is at least the largest cost, so that no part is empty).  Lengths live on the
 // device (a captured graph replays with other ones), so every CTA adds up the
 // list itself.  A job that one CTA owns whole is written out by it; of a job
 // cut at a range's end every CTA leaves one (m, l, o) record a row, and the
@@ -36,9 +39,9 @@ struct Request {
 
 // The job that holds a CTA's first tile, left for the combine kernel.
 struct CtaHeader {
-    int x_total;           // tiles of the whole call
-    int job_start;         // first tile of the job
-    int nt;                // its tiles
+    int x_total;           // cost of the whole call
+    int n_ranges;          // parts it is cut into
+    int job_start;         // where the job begins
     int b, hk, group;
     Request r;
     int pad[3];
@@ -60,6 +63,7 @@ struct TreeArgs {
     int KT;                              // key rows per tile
     int Lp, dtok, dsplit;                // depth tiles: rows a token takes, tokens per tile (Lw <= KT),
                                          // tiles per token (Lw > KT)
+    int cost1, cost2;                    // of a sequence tile of one row tile, of two; a depth tile: cost1
     int rec_rows, n_cta;
     float scale_log2;
 };
@@ -98,7 +102,17 @@ struct Job {
     Request r;
     int tok0, ntok;      // the group's tokens, relative to the request's first
     int nseq, ndep0, nt; // sequence tiles, depth tiles of the first Tq tokens, all tiles
+    int cseq, cost;      // cost of a sequence tile, of the job
 };
+// Where tile i of a job begins, and the first tile that begins at x or behind.
+__device__ __forceinline__ int tile_begin(const TreeArgs& a, const Job& j, int i) {
+    return min(i, j.nseq) * j.cseq + max(i - j.nseq, 0) * a.cost1;
+}
+__device__ __forceinline__ int tile_from(const TreeArgs& a, const Job& j, int x) {
+    if (x <= 0) return 0;
+    if (x <= j.nseq * j.cseq) return (x + j.cseq - 1) / j.cseq;
+    return min(j.nt, j.nseq + (x - j.nseq * j.cseq + a.cost1 - 1) / a.cost1);
+}
 
 __device__ __forceinline__ int groups_of(const TreeArgs& a, const Request& r) { return (r.n + a.Tg - 1) / a.Tg; }
 
@@ -111,21 +125,24 @@ __device__ __forceinline__ void set_group(const TreeArgs& a, Job& j, int group) 
     j.nseq = (keys + a.KT - 1) / a.KT;
     j.ndep0 = dep_tiles_of(a, min(j.ntok, a.Tq));
     j.nt = j.nseq + j.ndep0 + dep_tiles_of(a, j.ntok - a.Tq);
+    j.cseq = j.ntok > a.Tq ? a.cost2 : a.cost1;
+    j.cost = tile_begin(a, j, j.nt);
 }
 
-// Tiles of one KV head of a request.
-__device__ __forceinline__ int head_tiles(const TreeArgs& a, const Request& r) {
+// Cost of one KV head of a request.
+__device__ __forceinline__ int head_cost(const TreeArgs& a, const Request& r) {
     Job j;
     j.r = r;
     const int ng = groups_of(a, r);
     if (ng == 0) return 0;
     set_group(a, j, ng - 1);
-    int t = j.nt;
+    int t = j.cost;
     if (ng > 1) {                       // all groups but the last are alike, but for a chain's keys
         set_group(a, j, 0);
-        t += j.nt * (ng - 1);
+        t += j.cost * (ng - 1);
         if (!a.mask)
-            for (int g = 1; g < ng - 1; ++g) t += (r.held + (g + 1) * a.Tg + a.KT - 1) / a.KT - j.nseq;
+            for (int g = 1; g < ng - 1; ++g)
+                t += ((r.held + (g + 1) * a.Tg + a.KT - 1) / a.KT - j.nseq) * j.cseq;
     }
     return t;
 }
@@ -133,35 +150,38 @@ __device__ __forceinline__ int head_tiles(const TreeArgs& a, const Request& r) {
 // Where a CTA starts, in shared memory; written by schedule().
 struct Start {
     int warp_sum[32];
-    int b, hk, group, i0;    // first job and the first tile within it
+    int max_cost[32];
+    int b, hk, group;        // the job in which the CTA's part begins,
+    int lo;                  // and where in it
     Request r;
-    int count;               // tiles of this CTA
+    int length;              // of the part; 0: none
 };
 
-// First tile of range c of P over x tiles.
+// Where part c of P begins in a total of x.
 __device__ __forceinline__ int range_begin(int c, int x, int P) {
     const int q = x / P, rem = x - q * P;
     return c * q + min(c, rem);
 }
-// The range that holds tile t.
+// The part that holds x = t.
 __device__ __forceinline__ int range_of(int t, int x, int P) {
     const int q = x / P, rem = x - q * P;
     return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q;
 }
 
-// Called by all threads of the CTA: finds the CTA's range and writes its
-// header.  Ends with a __syncthreads.
+// Called by all threads of the CTA: finds the CTA's part and writes its header.
+// Ends with a __syncthreads.
 __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
     const int nth = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
     const int lane = tid & 31, warp = tid >> 5;
     const int ch = (a.B + nth - 1) / nth;
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
     Request r = {};
-    int ht = 0, mine = 0;
+    int hc = 0, mine = 0, most = a.cost1;
     for (int b = b0; b < b1; ++b) {
         r = load_request(a, b);
-        ht = head_tiles(a, r);
-        mine += ht * a.Hk;
+        hc = head_cost(a, r);
+        mine += hc * a.Hk;
+        if (r.n > a.Tq && a.Tg > a.Tq) most = a.cost2;
     }
     int inc = mine;
 #pragma unroll 1
@@ -169,16 +189,21 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
         const int up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
     }
-    if (lane == 31) s->warp_sum[warp] = inc;
-    if (tid == 0) s->count = 0;
+    most = __any_sync(0xffffffffu, most == a.cost2) ? a.cost2 : a.cost1;
+    if (lane == 31) {
+        s->warp_sum[warp] = inc;
+        s->max_cost[warp] = most;
+    }
+    if (tid == 0) s->length = 0;
     __syncthreads();
     int at = inc - mine, total = 0;
 #pragma unroll 1
     for (int w = 0; w < (nth >> 5); ++w) {
         if (w < warp) at += s->warp_sum[w];
         total += s->warp_sum[w];
+        most = max(most, s->max_cost[w]);
     }
-    const int P = min(a.n_cta, total), c = static_cast<int>(blockIdx.x);
+    const int P = min(a.n_cta, total / most), c = static_cast<int>(blockIdx.x);
     if (c < P) {
         const int lo = range_begin(c, total, P);
         if (at <= lo && lo < at + mine) {
@@ -186,31 +211,31 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
             if (ch > 1) {                // which of this thread's requests
                 for (;; ++b) {
                     r = load_request(a, b);
-                    ht = head_tiles(a, r);
-                    if (lo < at + ht * a.Hk) break;
-                    at += ht * a.Hk;
+                    hc = head_cost(a, r);
+                    if (lo < at + hc * a.Hk) break;
+                    at += hc * a.Hk;
                 }
             }
-            const int hk = (lo - at) / ht;
-            at += ht * hk;
+            const int hk = (lo - at) / hc;
+            at += hc * hk;
             Job j;
             j.r = r;
             int g = 0;
             for (;; ++g) {
                 set_group(a, j, g);
-                if (lo < at + j.nt) break;
-                at += j.nt;
+                if (lo < at + j.cost) break;
+                at += j.cost;
             }
             s->b = b;
             s->hk = hk;
             s->group = g;
-            s->i0 = lo - at;
+            s->lo = lo - at;
             s->r = r;
-            s->count = range_begin(c + 1, total, P) - lo;
-            a.hdr[c] = CtaHeader{total, at, j.nt, b, hk, g, r, {}};
+            s->length = range_begin(c + 1, total, P) - lo;
+            a.hdr[c] = CtaHeader{total, P, at, b, hk, g, r, {}};
         }
     } else if (tid == 0) {
-        a.hdr[c] = CtaHeader{total, 0, 0, 0, 0, 0, {}, {}};
+        a.hdr[c] = CtaHeader{total, P, 0, 0, 0, 0, {}, {}};
     }
     __syncthreads();
 }
@@ -221,22 +246,36 @@ struct Walk {
     Job j;
     RawRequest ahead;    // of request j.b + 1
     int i0, i1;          // this CTA's tiles of the job
-    int left;            // tiles left behind them
+    int end;             // where the CTA's part ends, from the job's beginning
     int seg;             // 0 for the first
     __device__ __forceinline__ bool begin(const TreeArgs& a, const Start& s) {
-        seg = 0;
-        left = s.count;
-        if (left <= 0) return false;
+        if (s.length == 0) return false;
         j.b = s.b;
         j.hk = s.hk;
         j.r = s.r;
         look_ahead(a);
         set_group(a, j, s.group);
-        take(s.i0);
-        return true;
+        end = s.lo + s.length;
+        take(a, tile_from(a, j, s.lo));
+        // the part may begin behind the job's last tile's beginning: then it has
+        // none of this job (nor does the combine kernel look for it)
+        seg = 0;
+        return i0 < i1 || next_job(a);
     }
     __device__ __forceinline__ bool next(const TreeArgs& a) {
-        if (left <= 0) return false;
+        ++seg;
+        return next_job(a);
+    }
+    // Whether this CTA owns the job whole (then it writes the outputs itself).
+    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == j.nt; }
+    // Where its record of a cut job goes: a job that began before the part is the
+    // part's first, one that begins in it and goes on is its last.
+    __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (i0 == 0); }
+
+   private:
+    __device__ __forceinline__ bool next_job(const TreeArgs& a) {
+        end -= j.cost;
+        if (end <= 0) return false;
         int g = j.group + 1;
         if (g * a.Tg >= j.r.n) {
             g = 0;
@@ -250,24 +289,15 @@ struct Walk {
             }
         }
         set_group(a, j, g);
-        ++seg;
-        take(0);
+        take(a, 0);
         return true;
     }
-    // Whether this CTA owns the job whole (then it writes the outputs itself).
-    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == j.nt; }
-    __device__ __forceinline__ int slot(const TreeArgs&) const {
-        return 2 * static_cast<int>(blockIdx.x) + (seg ? 1 : 0);
-    }
-
-   private:
     __device__ __forceinline__ void look_ahead(const TreeArgs& a) {
         if (j.b + 1 < a.B) ahead = load_raw(a, j.b + 1);
     }
-    __device__ __forceinline__ void take(int first) {
+    __device__ __forceinline__ void take(const TreeArgs& a, int first) {
         i0 = first;
-        i1 = min(j.nt, first + left);
-        left -= i1 - i0;
+        i1 = tile_from(a, j, end);
     }
 };
 
@@ -339,10 +369,10 @@ __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __f
 
 // Columns c0, c0 + step, ... (n of them) of output row `out`, stored before by the same thread.
 template <typename E, int D>
-__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Job j, int token, E* out, int c0, int step,
-                                            int n) {
+__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Request r, int b, int hk, int token, E* out,
+                                            int c0, int step, int n) {
     const int page = 1 << a.page_shift;
-    const size_t row = (static_cast<size_t>(j.r.cu0 + token) * a.Hk + j.hk) * a.L;
+    const size_t row = (static_cast<size_t>(r.cu0 + token) * a.Hk + hk) * a.L;
     for (int x = 0; x < n; ++x) {
         const int col = c0 + x * step;
         float sum = to_float(out[col]);
@@ -350,13 +380,13 @@ __device__ __noinline__ void add_not_finite(const TreeArgs& a, const Job j, int 
             const float v = to_float(*p);
             if (!isfinite(v)) sum += v;
         };
-        for (int k = 0; k < j.r.n; ++k) {
-            const int key = j.r.held + k;
-            if (!(seq_visible(a, j.r, token, key) & 1u)) continue;
-            const int p = page_of(a, j.b, key);
+        for (int k = 0; k < r.n; ++k) {
+            const int key = r.held + k;
+            if (!(seq_visible(a, r, token, key) & 1u)) continue;
+            const int p = page_of(a, b, key);
             if (p < 0) continue;
             add(static_cast<const E*>(a.vc) +
-                ((static_cast<size_t>(p) * a.Hk + j.hk) * page + (key & (page - 1))) * D + col);
+                ((static_cast<size_t>(p) * a.Hk + hk) * page + (key & (page - 1))) * D + col);
         }
         for (int l = a.win_lo; l < a.L; ++l) add(static_cast<const E*>(a.vd) + (row + l) * D + col);
         from_float(out + col, sum);

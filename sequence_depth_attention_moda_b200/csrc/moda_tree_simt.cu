@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
         __syncthreads();
         const bool poison = *spoison != 0;
         const bool whole = w.whole();
-        const size_t slot = w.slot(a);
+        const size_t slot = w.slot();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 4 * rg + r;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
                     float* out = static_cast<float*>(a.o) + orow * D;
                     *reinterpret_cast<float4*>(out + col) =
                         make_float4(o[r][c][0] * inv, o[r][c][1] * inv, o[r][c][2] * inv, o[r][c][3] * inv);
-                    if (poison) add_not_finite<float, D>(a, j, tk, out, col, 1, 4);
+                    if (poison) add_not_finite<float, D>(a, j.r, j.b, j.hk, tk, out, col, 1, 4);
                 }
                 if (cg == 0) a.lse[orow] = row_lse(mr, lr);
             } else {
@@ -318,18 +318,20 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const CtaHeader h = a.hdr[c];
-    const int P = min(a.n_cta, h.x_total);
+    const int P = h.n_ranges;
     if (c >= P) return;
-    const int prev = range_begin(c - 1, h.x_total, P);
-    if (h.job_start >= range_begin(c, h.x_total, P) || h.job_start < prev) return;
-    // records: range c-1 (slot 0 if the job is its first), then slot 0 of each range that begins inside the job
-    const int n = range_of(h.job_start + h.nt - 1, h.x_total, P) - c + 2;
-    auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(c - 1 + i) + (i == 0 && h.job_start > prev); };
     Job j;
     j.b = h.b;
     j.hk = h.hk;
     j.r = h.r;
     set_group(a, j, h.group);
+    // The parts that hold the beginnings of the job's first and last tile.  Part c
+    // is the one to work if it is the second of several.
+    const int first = range_of(h.job_start, h.x_total, P);
+    const int last = range_of(h.job_start + tile_begin(a, j, j.nt - 1), h.x_total, P);
+    if (c != first + 1 || last == first) return;
+    const int n = last - first + 1;
+    auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(first + i) + (i == 0); };   // see Walk::slot
     for (int row = blockIdx.y * kCombineWarps + warp; row < j.ntok * a.G; row += gridDim.y * kCombineWarps) {
         // online over the records, kBatch of them in flight at a time
         float M = -INFINITY, l = 0.0f, acc[C] = {};
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
         for (int e = 0; e < C; ++e) from_float(static_cast<E*>(a.o) + orow * D + lane + 32 * e, acc[e] * inv);
-        if (poison) add_not_finite<E, D>(a, j, tk, static_cast<E*>(a.o) + orow * D, lane, 32, C);
+        if (poison) add_not_finite<E, D>(a, j.r, j.b, j.hk, tk, static_cast<E*>(a.o) + orow * D, lane, 32, C);
         if (lane == 0) a.lse[orow] = row_lse(ref, l);
     }
 }

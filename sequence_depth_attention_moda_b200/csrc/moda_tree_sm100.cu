@@ -54,6 +54,20 @@ constexpr float kLazy = 8.0f;                // log2 by which a maximum may pass
 constexpr int kMarks = 2;                    // segments whose marks are told apart: a warp marks segment k+1
                                              // only when all have begun to write out segment k
 
+// A segment: the tiles of one job that this CTA owns.  Warp 0 walks the jobs and
+// publishes their segments in a ring in shared memory, so that the walk's code
+// and its reads of lengths exist once.  Warp 0 is ahead of the slowest role by at
+// most a K ring and the S buffers in tiles, each of which may be a segment: the
+// ring is longer than that, and no one has to say that a segment is done with.
+struct Seg {
+    Request r;
+    int b, hk, tok0, ntok, nseq, ndep0, keys;
+    int i0, i1;          // its tiles; i1 < 0: there are no more segments
+    int whole, slot;     // see Walk
+    int pad[2];
+};
+constexpr int kSegs = 16;
+
 // NQ: query tiles of a job, and O accumulators.
 template <int D, int NQ>
 struct Lay {
@@ -71,13 +85,15 @@ struct Lay {
     // barrier indexes; from kPReady on they take an arrival of each softmax warp
     static constexpr int kQFull = 0, kQFree = NQ, kKFull = 2 * NQ, kKEmpty = kKFull + kKS, kVFull = kKEmpty + kKS,
                          kVEmpty = kVFull + kVS, kSFull = kVEmpty + kVS, kSFree = kSFull + kNS,
-                         kOFull = kSFree + kNS, kPReady = kOFull + NQ, kOFree = kPReady + kNS, kNumBars = kOFree + NQ;
+                         kOFull = kSFree + kNS, kSegFull = kOFull + NQ, kPReady = kSegFull + kSegs, kOFree = kPReady + kNS, kNumBars = kOFree + NQ;
     static constexpr uint32_t kStart = kBar + (kNumBars * 8 + 15) / 16 * 16;
-    static constexpr uint32_t kMisc = kStart + (sizeof(Start) + 15) / 16 * 16;  // tmem base, abort flag, marks
+    static constexpr uint32_t kSeg = kStart + (sizeof(Start) + 15) / 16 * 16;
+    static constexpr uint32_t kMisc = kSeg + kSegs * sizeof(Seg);       // tmem base, abort flag, marks
     static constexpr uint32_t kBytes = kMisc + 16 + kMarks * 4;
     static constexpr uint32_t kDynSmem = kBytes + 1024;     // alignment slack
     static_assert(kColO + NQ * D <= kTmemCols, "TMEM columns");
     static_assert(kDynSmem <= 232448, "shared memory of one CTA");
+    static_assert(kKS + kNS + 2 < kSegs && kVS + 2 < kSegs, "segments in flight");
 };
 
 struct SmArgs {
@@ -86,7 +102,7 @@ struct SmArgs {
     int box_rows;        // rows of a cache box: min(page, 128)
 };
 
-// What the MMA and softmax roles derive alike while they walk the CTA's tiles.
+// What the MMA and softmax roles derive alike while they go through the CTA's tiles.
 // A slot is a query tile's place: shared memory for Q, TMEM for O.  Jobs of one
 // query tile take the slots in turn.
 template <int NQ>
@@ -98,8 +114,8 @@ struct Roles {
     bool two;            // two query tiles
     int first;           // slots first .. last
     int last;
-    __device__ __forceinline__ void segment(const TreeArgs& a, const Walk& w) {
-        two = NQ == 2 && w.j.ntok > a.Tq;
+    __device__ __forceinline__ void segment(const TreeArgs& a, const Seg& g) {
+        two = NQ == 2 && g.ntok > a.Tq;
         first = two ? 0 : turn;
         last = two ? 1 : turn;
     }
@@ -107,8 +123,8 @@ struct Roles {
     // Query tile of slot s.
     __device__ __forceinline__ int sub(int s) const { return two ? s : 0; }
     // Whether slot s takes the job's tile i.
-    __device__ __forceinline__ bool takes(const Walk& w, int i, int s) const {
-        return !two || i < w.j.nseq || (i >= w.j.nseq + w.j.ndep0) == (s == 1);
+    __device__ __forceinline__ bool takes(const Seg& g, int i, int s) const {
+        return !two || i < g.nseq || (i >= g.nseq + g.ndep0) == (s == 1);
     }
     __device__ __forceinline__ void end_segment() {
         used0 += first == 0;
@@ -119,25 +135,21 @@ struct Roles {
     }
 };
 
-// Sequence keys of a job.
-__device__ __forceinline__ int job_keys(const TreeArgs& a, const Job& j) {
-    return j.r.held + (a.mask ? j.r.n : j.tok0 + j.ntok);
-}
 // A depth tile's query tile, its index there, and a query tile's tokens.
-__device__ __forceinline__ int dep_sub(const Walk& w, int i) { return i >= w.j.nseq + w.j.ndep0 ? 1 : 0; }
-__device__ __forceinline__ int dep_index(const Walk& w, int i) {
-    const int dt = i - w.j.nseq;
-    return dt < w.j.ndep0 ? dt : dt - w.j.ndep0;
+__device__ __forceinline__ int dep_sub(const Seg& g, int i) { return i >= g.nseq + g.ndep0 ? 1 : 0; }
+__device__ __forceinline__ int dep_index(const Seg& g, int i) {
+    const int dt = i - g.nseq;
+    return dt < g.ndep0 ? dt : dt - g.ndep0;
 }
-__device__ __forceinline__ int sub_tokens(const TreeArgs& a, const Job& j, int sub) {
-    return sub == 0 ? min(j.ntok, a.Tq) : j.ntok - a.Tq;
+__device__ __forceinline__ int sub_tokens(const TreeArgs& a, const Seg& g, int sub) {
+    return sub == 0 ? min(g.ntok, a.Tq) : g.ntok - a.Tq;
 }
 
 // Rows of tile i from its first on that its products have to cover.
-__device__ __forceinline__ int tile_rows(const TreeArgs& a, const Walk& w, int i) {
-    if (i < w.j.nseq) return min(kTile, job_keys(a, w.j) - i * kTile);
-    const int dt = dep_index(w, i);
-    if (a.Lw <= kTile) return min(a.dtok, sub_tokens(a, w.j, dep_sub(w, i)) - dt * a.dtok) * a.Lp;
+__device__ __forceinline__ int tile_rows(const TreeArgs& a, const Seg& g, int i) {
+    if (i < g.nseq) return min(kTile, g.keys - i * kTile);
+    const int dt = dep_index(g, i);
+    if (a.Lw <= kTile) return min(a.dtok, sub_tokens(a, g, dep_sub(g, i)) - dt * a.dtok) * a.Lp;
     return min(kTile, a.Lw - dt % a.dsplit * kTile);
 }
 
@@ -149,44 +161,44 @@ struct Box {
     uint32_t bytes;      // of the whole tile
 };
 // Table entry for this lane's box of tile i (0 where it has none).
-__device__ __forceinline__ int box_entry(const TreeArgs& a, int box_rows, const Walk& w, int i, int lane) {
-    if (i >= min(w.i1, w.j.nseq) || lane * box_rows >= min(kTile, job_keys(a, w.j) - i * kTile)) return 0;
-    return table_entry(a, w.j.b, i * kTile + lane * box_rows);
+__device__ __forceinline__ int box_entry(const TreeArgs& a, int box_rows, const Seg& g, int i, int lane) {
+    if (i >= min(g.i1, g.nseq) || lane * box_rows >= min(kTile, g.keys - i * kTile)) return 0;
+    return table_entry(a, g.b, i * kTile + lane * box_rows);
 }
-__device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Walk& w, int i, int entry,
+__device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int slabs, const Seg& g, int i, int entry,
                                         int lane) {
     Box x;
-    x.dep = i >= w.j.nseq;
-    x.once = x.dep || w.j.r.n <= a.Tg;   // one group: no other job reads these keys
+    x.dep = i >= g.nseq;
+    x.once = x.dep || g.r.n <= a.Tg;   // one group: no other job reads these keys
     x.mine = false;
     x.c1 = x.c2 = x.row = 0;
     if (!x.dep) {
         const int key = i * kTile + lane * box_rows;
-        const int left = min(kTile, job_keys(a, w.j) - i * kTile);
+        const int left = min(kTile, g.keys - i * kTile);
         x.mine = lane * box_rows < left;
         x.bytes = ((left + box_rows - 1) / box_rows) * box_rows * 128u * slabs;
         if (x.mine) {
             const int p = checked_page(a, entry);
             x.row = lane * box_rows;
             x.c1 = key & ((1 << a.page_shift) - 1);
-            x.c2 = p < 0 ? -1 : p * a.Hk + w.j.hk;      // outside: the box reads as zeros
+            x.c2 = p < 0 ? -1 : p * a.Hk + g.hk;      // outside: the box reads as zeros
         }
         return x;
     }
-    const int sub = dep_sub(w, i), dt = dep_index(w, i);
-    const int tok = w.j.r.cu0 + w.j.tok0 + sub * a.Tq;
+    const int sub = dep_sub(g, i), dt = dep_index(g, i);
+    const int tok = g.r.cu0 + g.tok0 + sub * a.Tq;
     if (a.Lw <= kTile) {
-        const int cnt = min(a.dtok, sub_tokens(a, w.j, sub) - dt * a.dtok);
+        const int cnt = min(a.dtok, sub_tokens(a, g, sub) - dt * a.dtok);
         x.mine = lane < cnt;
         x.bytes = cnt * a.Lw * 128u * slabs;
         x.row = lane * a.Lp;
         x.c1 = a.win_lo;
-        x.c2 = (tok + dt * a.dtok + lane) * a.Hk + w.j.hk;
+        x.c2 = (tok + dt * a.dtok + lane) * a.Hk + g.hk;
     } else {
         x.mine = lane == 0;
         x.bytes = kTile * 128u * slabs;                 // rows behind the last depth row read as zeros
         x.c1 = a.win_lo + dt % a.dsplit * kTile;
-        x.c2 = (tok + dt / a.dsplit) * a.Hk + w.j.hk;
+        x.c2 = (tok + dt / a.dsplit) * a.Hk + g.hk;
     }
     return x;
 }
@@ -326,7 +338,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             mbar_wait(&bars[full + x % stages], (x / stages) & 1, a.status, &no_abort);
     };
 
-    Walk w;
+    Seg* segs = reinterpret_cast<Seg*>(smem + L::kSeg);
+    Seg sg;
+    int k = -1;              // segment
+    // the next segment, or false; for a whole warp, and for one thread
+    auto next_seg_all = [&]() -> bool {
+        ++k;
+        if (!wait_all(L::kSegFull + k % kSegs, k / kSegs)) return false;
+        sg = segs[k % kSegs];
+        return sg.i1 >= 0;
+    };
+    auto next_seg_one = [&]() -> bool {
+        ++k;
+        if (!wait(L::kSegFull + k % kSegs, k / kSegs)) return false;
+        sg = segs[k % kSegs];
+        return sg.i1 >= 0;
+    };
     Roles<NQ> r;
     // 384 threads of 168 registers: 128 x 104 + 256 x 200, or 128 x 88 + 256 x 208
     // (two query tiles' statistics); local memory has next to no L1 beside this
@@ -337,8 +364,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         // ------------------------------------------------- producer of Q, K --
         const uint32_t q_bytes = L::kSlabs * 128u * a.Tq * a.G;
         bool ok = true;
-        for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
-            r.segment(a, w);
+        Walk w;
+        for (bool more = w.begin(a, *start); ok; more = w.next(a)) {
+            ++k;
+            sg.r = w.j.r;
+            sg.b = w.j.b;
+            sg.hk = w.j.hk;
+            sg.tok0 = w.j.tok0;
+            sg.ntok = w.j.ntok;
+            sg.nseq = w.j.nseq;
+            sg.ndep0 = w.j.ndep0;
+            sg.keys = w.j.r.held + (a.mask ? w.j.r.n : w.j.tok0 + w.j.ntok);
+            sg.i0 = w.i0;
+            sg.i1 = more ? w.i1 : -1;
+            sg.whole = w.whole();
+            sg.slot = w.slot();
+            if (lane == 0) {
+                segs[k % kSegs] = sg;
+                mbar_arrive(&bars[L::kSegFull + k % kSegs]);
+            }
+            __syncwarp();
+            if (!more) break;
+            r.segment(a, sg);
             for (int s = r.first; s <= r.last; ++s) {
                 if (r.used(s) > 0 && !wait_all(L::kQFree + s, r.used(s) - 1)) {
                     ok = false;
@@ -348,16 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     mbar_arrive_expect_tx(&bars[L::kQFull + s], q_bytes);
                     for (int x = 0; x < L::kSlabs; ++x)
                         tma_load_3d(smem + L::kQ + s * L::kTileBytes + x * kSlab, &g.tq, &bars[L::kQFull + s], x * 64,
-                                    w.j.hk * a.G, w.j.r.cu0 + w.j.tok0 + r.sub(s) * a.Tq);
+                                    sg.hk * a.G, sg.r.cu0 + sg.tok0 + r.sub(s) * a.Tq);
                 }
             }
             if (!ok) break;
             // table entries two tiles ahead: under load a read takes as long as a tile
-            int e0 = box_entry(a, g.box_rows, w, w.i0, lane), e1 = box_entry(a, g.box_rows, w, w.i0 + 1, lane);
-            for (int i = w.i0; i < w.i1; ++i, ++r.j) {
-                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, e0, lane);
+            int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
+            for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
+                const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
                 e0 = e1;
-                e1 = box_entry(a, g.box_rows, w, i + 2, lane);
+                e1 = box_entry(a, g.box_rows, sg, i + 2, lane);
                 const int st = r.j % L::kKS;
                 if (r.j >= L::kKS && !wait_all(L::kKEmpty + st, r.j / L::kKS - 1)) {
                     ok = false;
@@ -375,12 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
     } else if (warp == 1) {
         // ------------------------------------------------- producer of V -----
         bool ok = true;
-        for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
-            int e0 = box_entry(a, g.box_rows, w, w.i0, lane), e1 = box_entry(a, g.box_rows, w, w.i0 + 1, lane);
-            for (int i = w.i0; i < w.i1; ++i, ++r.j) {
-                const Box x = tile_box(a, g.box_rows, L::kSlabs, w, i, e0, lane);
+        while (ok && next_seg_all()) {
+            int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
+            for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
+                const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
                 e0 = e1;
-                e1 = box_entry(a, g.box_rows, w, i + 2, lane);
+                e1 = box_entry(a, g.box_rows, sg, i + 2, lane);
                 const int st = r.j % L::kVS;
                 if (r.j >= L::kVS && !wait_all(L::kVEmpty + st, r.j / L::kVS - 1)) {
                     ok = false;
@@ -397,14 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             const uint64_t qd = desc_kmajor_sw128(smem_u32(smem + L::kQ));
             const uint64_t kd = desc_kmajor_sw128(smem_u32(smem + L::kK));
             bool ok = true;
-            for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
-                r.segment(a, w);
+            while (ok && next_seg_one()) {
+                r.segment(a, sg);
                 for (int s = r.first; ok && s <= r.last; ++s) ok = wait(L::kQFull + s, r.used(s));
-                for (int i = w.i0; ok && i < w.i1; ++i, ++r.j) {
+                for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
                     const int st = r.j % L::kKS;
                     if (!(ok = wait(L::kKFull + st, r.j / L::kKS))) break;
                     for (int s = r.first; s <= r.last; ++s) {
-                        if (!r.takes(w, i, s)) continue;
+                        if (!r.takes(sg, i, s)) continue;
                         // the buffer holds P of block b - kNS until its P V is done
                         const int sb = r.b % L::kNS;
                         if (r.b >= L::kNS && !(ok = wait(L::kSFree + sb, r.b / L::kNS - 1))) break;
@@ -433,18 +480,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             const uint32_t id = idesc_bf16(128, D, false, true);
             const uint64_t vd = desc_mnmajor_sw128(smem_u32(smem + L::kV), kSlab);
             bool ok = true;
-            for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
-                r.segment(a, w);
+            while (ok && next_seg_one()) {
+                r.segment(a, sg);
                 // the slots' accumulators must have been read out
                 for (int s = r.first; ok && s <= r.last; ++s)
                     if (r.used(s) > 0) ok = wait(L::kOFree + s, r.used(s) - 1);
                 int begun = 0;                        // slots with a product in this segment (bits)
-                for (int i = w.i0; ok && i < w.i1; ++i, ++r.j) {
+                for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
                     const int st = r.j % L::kVS;
-                    const int steps = (tile_rows(a, w, i) + 15) / 16;     // 16 keys each
+                    const int steps = (tile_rows(a, sg, i) + 15) / 16;     // 16 keys each
                     if (!(ok = wait(L::kVFull + st, r.j / L::kVS))) break;
                     for (int s = r.first; s <= r.last; ++s) {
-                        if (!r.takes(w, i, s)) continue;
+                        if (!r.takes(sg, i, s)) continue;
                         const int sb = r.b % L::kNS;
                         if (!(ok = wait(L::kPReady + sb, r.b / L::kNS))) break;
                         tc_fence_after();
@@ -484,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(row0) << 16);
         const float sl2 = a.scale_log2;
         bool ok = true;
-        for (bool more = w.begin(a, *start); ok && more; more = w.next(a)) {
-            r.segment(a, w);
+        while (ok && next_seg_all()) {
+            r.segment(a, sg);
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // per slot; l: this half's share
             int prev0 = -1, prev1 = -1;               // the slot's last block in this segment
-            const int n_tok0 = sub_tokens(a, w.j, 0), n_tok1 = r.two ? sub_tokens(a, w.j, 1) : n_tok0;
+            const int n_tok0 = sub_tokens(a, sg, 0), n_tok1 = r.two ? sub_tokens(a, sg, 1) : n_tok0;
             // One block: slot s, tile i; `masks`: some key of the tile is hidden from some row.
             // `clean`: the tile's values are looked over here (a tile's first block does).
             auto block = [&](auto masks, int i, int s, int n_tok, float& m, float& l, int& prev, bool clean) -> bool {
@@ -504,24 +551,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;   // of this thread's 64 columns
                     bool blind = false;               // none of the warp's tokens is in this depth tile
                     if constexpr (kMasks) {
-                        const bool dep = i >= w.j.nseq;
+                        const bool dep = i >= sg.nseq;
                         if (real) {
                             const int c = half * 64;
                             if (dep) {
-                                const int dt = dep_index(w, i);
+                                const int dt = dep_index(sg, i);
                                 vis0 = dep_visible(a, t_off, dt, c);
                                 vis1 = dep_visible(a, t_off, dt, c + 32);
                             } else {
-                                const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
-                                const int rel = i * kTile + c - w.j.r.held;
+                                const int token = sg.tok0 + r.sub(s) * a.Tq + t_off;
+                                const int rel = i * kTile + c - sg.r.held;
                                 if (a.mask) {
                                     const uint2 v = mask_visible64(
-                                        a.mask + static_cast<size_t>(w.j.r.cu0 + token) * a.words, a.words, w.j.r.n, rel);
+                                        a.mask + static_cast<size_t>(sg.r.cu0 + token) * a.words, a.words, sg.r.n, rel);
                                     vis0 = v.x;
                                     vis1 = v.y;
                                 } else {
-                                    vis0 = chain_visible(w.j.r.n, token, rel);
-                                    vis1 = chain_visible(w.j.r.n, token, rel + 32);
+                                    vis0 = chain_visible(sg.r.n, token, rel);
+                                    vis1 = chain_visible(sg.r.n, token, rel + 32);
                                 }
                             }
                         }
@@ -600,12 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     if (clean) {
                         const int st = r.j % L::kVS;
                         if (!wait_all(L::kVFull + st, r.j / L::kVS)) return false;
-                        const bool dep = i >= w.j.nseq;
+                        const bool dep = i >= sg.nseq;
                         const bool bad = clean_values<D>(smem + L::kV + st * L::kTileBytes, (warp - 4) * 16,
-                                                         tile_rows(a, w, i), dep ? 0 : w.j.r.held - i * kTile,
+                                                         tile_rows(a, sg, i), dep ? 0 : sg.r.held - i * kTile,
                                                          dep && a.Lw <= kTile ? a.Lp : kTile,
                                                          dep && a.Lw <= kTile ? a.Lw : kTile);
-                        if (bad && lane == 0) marks[w.seg % kMarks] = w.seg + 1;
+                        if (bad && lane == 0) marks[k % kMarks] = k + 1;
                     }
                 }
                 tc_fence_before();
@@ -614,17 +661,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 prev = r.b++;
                 return true;
             };
-            int i = w.i0;
-            const int open = min(w.i1, w.j.r.held / kTile);       // tiles of held keys alone
+            int i = sg.i0;
+            const int open = min(sg.i1, sg.r.held / kTile);       // tiles of held keys alone
             for (; ok && i < open; ++i, ++r.j) {
                 if (r.first == 0) ok = block(std::false_type{}, i, 0, n_tok0, m0, l0, prev0, false);
                 if (NQ == 2 && ok && r.last == 1) ok = block(std::false_type{}, i, 1, n_tok1, m1, l1, prev1, false);
             }
-            for (; ok && i < w.i1; ++i, ++r.j) {
+            for (; ok && i < sg.i1; ++i, ++r.j) {
                 bool clean = true;
 #pragma unroll 1
                 for (int s = r.first; ok && s <= r.last; ++s) {
-                    if (!r.takes(w, i, s)) continue;
+                    if (!r.takes(sg, i, s)) continue;
                     float m = s ? m1 : m0, l = s ? l1 : l0;
                     int prev = s ? prev1 : prev0;
                     ok = block(std::true_type{}, i, s, s ? n_tok1 : n_tok0, m, l, prev, clean);
@@ -634,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 }
             }
             // ------------------------------------------------ end of segment --
-            const bool whole = w.whole();
+            const bool whole = sg.whole != 0;
 #pragma unroll 1
             for (int s = r.first; ok && s <= r.last; ++s) {
                 if (!wait_all(L::kOFull + s, r.used(s))) {
@@ -643,13 +690,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 }
                 const float m = s ? m1 : m0, l = s ? l1 : l0;
                 tc_fence_after();
-                const int n_tok = sub_tokens(a, w.j, r.sub(s));
+                const int n_tok = sub_tokens(a, sg, r.sub(s));
                 const bool real = t_off < n_tok && t_off < a.Tq;
-                const bool poison = marks[w.seg % kMarks] == w.seg + 1;
+                const bool poison = marks[k % kMarks] == k + 1;
                 const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
-                const int token = w.j.tok0 + r.sub(s) * a.Tq + t_off;
-                const size_t orow = static_cast<size_t>(w.j.r.cu0 + token) * a.Hq + w.j.hk * a.G + (row - t_off * a.G);
-                const size_t rec = static_cast<size_t>(w.slot(a)) * a.rec_rows + r.sub(s) * a.Tq * a.G + row;
+                const int token = sg.tok0 + r.sub(s) * a.Tq + t_off;
+                const size_t orow = static_cast<size_t>(sg.r.cu0 + token) * a.Hq + sg.hk * a.G + (row - t_off * a.G);
+                const size_t rec = static_cast<size_t>(sg.slot) * a.rec_rows + r.sub(s) * a.Tq * a.G + row;
                 const bool some = row0 < n_tok * a.G && (s ? prev1 : prev0) >= 0;    // O of these rows was written
                 uint32_t o[D / 2];
                 if (some) {
@@ -675,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                         dst[c / 8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                                                 pack_bf16(v[6], v[7]));
                     }
-                    if (poison) add_not_finite<__nv_bfloat16, D>(a, w.j, token, out, half * (D / 2), 1, D / 2);
+                    if (poison) add_not_finite<__nv_bfloat16, D>(a, sg.r, sg.b, sg.hk, token, out, half * (D / 2), 1, D / 2);
                     if (half == 0) a.lse[orow] = row_lse(m, lt);
                 } else {
                     if (some) {
