@@ -695,8 +695,8 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         a.B = p.B; a.N = p.N; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.G; a.L = p.L; a.Lw = p.Lw; a.win_lo = p.win_lo;
         a.page_shift = p.page_shift; a.n_pages = p.n_pages; a.max_pages = p.max_pages; a.words = p.words;
         a.Tq = t.Tq; a.Tg = t.Tg; a.KT = t.KT; a.Lp = t.Lp; a.dtok = t.dtok; a.dsplit = t.dsplit;
-        a.cost1 = 1;
-        a.cost2 = t.tiles;
+        a.two_cost = t.tiles;
+        while ((1 << a.kt_shift) < t.KT) ++a.kt_shift;
         a.rec_rows = t.rec_rows; a.n_cta = t.n_cta; a.scale_log2 = p.scale_log2;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         phase_mark(0, s);

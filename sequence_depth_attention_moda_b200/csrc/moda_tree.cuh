@@ -60,10 +60,10 @@ struct TreeArgs {
     int B, N, Hq, Hk, G, L, Lw, win_lo;  // Lw: depth rows in the window
     int page_shift, n_pages, max_pages, words;
     int Tq, Tg;                          // tokens per row tile, per job (Tg = Tq or 2*Tq)
-    int KT;                              // key rows per tile
+    int kt_shift, KT;                    // key rows per tile, a power of two
     int Lp, dtok, dsplit;                // depth tiles: rows a token takes, tokens per tile (Lw <= KT),
                                          // tiles per token (Lw > KT)
-    int cost1, cost2;                    // of a sequence tile of one row tile, of two; a depth tile: cost1
+    int two_cost;                        // cost of a sequence tile that two row tiles take: 1 or 2 (others: 1)
     int rec_rows, n_cta;
     float scale_log2;
 };
@@ -94,7 +94,8 @@ __device__ __forceinline__ Request load_request(const TreeArgs& a, int b) { retu
 
 __device__ __forceinline__ int dep_tiles_of(const TreeArgs& a, int tokens) {
     if (a.Lw == 0 || tokens <= 0) return 0;
-    return a.Lw <= a.KT ? (tokens + a.dtok - 1) / a.dtok : tokens * a.dsplit;
+    if (a.Lw > a.KT) return tokens * a.dsplit;
+    return tokens <= a.dtok ? 1 : (tokens + a.dtok - 1) / a.dtok;
 }
 
 struct Job {
@@ -102,19 +103,21 @@ struct Job {
     Request r;
     int tok0, ntok;      // the group's tokens, relative to the request's first
     int nseq, ndep0, nt; // sequence tiles, depth tiles of the first Tq tokens, all tiles
-    int cseq, cost;      // cost of a sequence tile, of the job
+    int cseq, cost;      // cost of a sequence tile (1 or 2), of the job
 };
 // Where tile i of a job begins, and the first tile that begins at x or behind.
-__device__ __forceinline__ int tile_begin(const TreeArgs& a, const Job& j, int i) {
-    return min(i, j.nseq) * j.cseq + max(i - j.nseq, 0) * a.cost1;
+__device__ __forceinline__ int tile_begin(const Job& j, int i) {
+    return i + min(i, j.nseq) * (j.cseq - 1);
 }
-__device__ __forceinline__ int tile_from(const TreeArgs& a, const Job& j, int x) {
+__device__ __forceinline__ int tile_from(const Job& j, int x) {
     if (x <= 0) return 0;
-    if (x <= j.nseq * j.cseq) return (x + j.cseq - 1) / j.cseq;
-    return min(j.nt, j.nseq + (x - j.nseq * j.cseq + a.cost1 - 1) / a.cost1);
+    if (x <= j.nseq * j.cseq) return (x + j.cseq - 1) >> (j.cseq - 1);
+    return min(j.nt, x - j.nseq * (j.cseq - 1));
 }
 
-__device__ __forceinline__ int groups_of(const TreeArgs& a, const Request& r) { return (r.n + a.Tg - 1) / a.Tg; }
+__device__ __forceinline__ int groups_of(const TreeArgs& a, const Request& r) {
+    return r.n <= a.Tg ? (r.n > 0) : (r.n + a.Tg - 1) / a.Tg;
+}
 
 __device__ __forceinline__ void set_group(const TreeArgs& a, Job& j, int group) {
     j.group = group;
@@ -122,11 +125,11 @@ __device__ __forceinline__ void set_group(const TreeArgs& a, Job& j, int group) 
     j.ntok = min(a.Tg, j.r.n - j.tok0);
     // a chain's group sees no key behind its last token
     const int keys = j.r.held + (a.mask ? j.r.n : j.tok0 + j.ntok);
-    j.nseq = (keys + a.KT - 1) / a.KT;
+    j.nseq = (keys + a.KT - 1) >> a.kt_shift;
     j.ndep0 = dep_tiles_of(a, min(j.ntok, a.Tq));
     j.nt = j.nseq + j.ndep0 + dep_tiles_of(a, j.ntok - a.Tq);
-    j.cseq = j.ntok > a.Tq ? a.cost2 : a.cost1;
-    j.cost = tile_begin(a, j, j.nt);
+    j.cseq = j.ntok > a.Tq ? a.two_cost : 1;
+    j.cost = j.nt + j.nseq * (j.cseq - 1);
 }
 
 // Cost of one KV head of a request.
@@ -142,7 +145,7 @@ __device__ __forceinline__ int head_cost(const TreeArgs& a, const Request& r) {
         t += j.cost * (ng - 1);
         if (!a.mask)
             for (int g = 1; g < ng - 1; ++g)
-                t += ((r.held + (g + 1) * a.Tg + a.KT - 1) / a.KT - j.nseq) * j.cseq;
+                t += (((r.held + (g + 1) * a.Tg + a.KT - 1) >> a.kt_shift) - j.nseq) * j.cseq;
     }
     return t;
 }
@@ -151,9 +154,8 @@ __device__ __forceinline__ int head_cost(const TreeArgs& a, const Request& r) {
 struct Start {
     int warp_sum[32];
     int max_cost[32];
-    int b, hk, group;        // the job in which the CTA's part begins,
+    Job j;                   // the job in which the CTA's part begins,
     int lo;                  // and where in it
-    Request r;
     int length;              // of the part; 0: none
 };
 
@@ -176,12 +178,12 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
     const int ch = (a.B + nth - 1) / nth;
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
     Request r = {};
-    int hc = 0, mine = 0, most = a.cost1;
+    int hc = 0, mine = 0, most = 1;
     for (int b = b0; b < b1; ++b) {
         r = load_request(a, b);
         hc = head_cost(a, r);
         mine += hc * a.Hk;
-        if (r.n > a.Tq && a.Tg > a.Tq) most = a.cost2;
+        if (r.n > a.Tq) most = a.two_cost;
     }
     int inc = mine;
 #pragma unroll 1
@@ -189,7 +191,7 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
         const int up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
     }
-    most = __any_sync(0xffffffffu, most == a.cost2) ? a.cost2 : a.cost1;
+    most = 1 + __any_sync(0xffffffffu, most > 1);
     if (lane == 31) {
         s->warp_sum[warp] = inc;
         s->max_cost[warp] = most;
@@ -220,17 +222,16 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
             at += hc * hk;
             Job j;
             j.r = r;
+            j.b = b;
+            j.hk = hk;
             int g = 0;
             for (;; ++g) {
                 set_group(a, j, g);
                 if (lo < at + j.cost) break;
                 at += j.cost;
             }
-            s->b = b;
-            s->hk = hk;
-            s->group = g;
+            s->j = j;
             s->lo = lo - at;
-            s->r = r;
             s->length = range_begin(c + 1, total, P) - lo;
             a.hdr[c] = CtaHeader{total, P, at, b, hk, g, r, {}};
         }
@@ -250,13 +251,10 @@ struct Walk {
     int seg;             // 0 for the first
     __device__ __forceinline__ bool begin(const TreeArgs& a, const Start& s) {
         if (s.length == 0) return false;
-        j.b = s.b;
-        j.hk = s.hk;
-        j.r = s.r;
+        j = s.j;
         look_ahead(a);
-        set_group(a, j, s.group);
         end = s.lo + s.length;
-        take(a, tile_from(a, j, s.lo));
+        take(tile_from(j, s.lo));
         // the part may begin behind the job's last tile's beginning: then it has
         // none of this job (nor does the combine kernel look for it)
         seg = 0;
@@ -289,15 +287,15 @@ struct Walk {
             }
         }
         set_group(a, j, g);
-        take(a, 0);
+        take(0);
         return true;
     }
     __device__ __forceinline__ void look_ahead(const TreeArgs& a) {
         if (j.b + 1 < a.B) ahead = load_raw(a, j.b + 1);
     }
-    __device__ __forceinline__ void take(const TreeArgs& a, int first) {
+    __device__ __forceinline__ void take(int first) {
         i0 = first;
-        i1 = tile_from(a, j, end);
+        i1 = tile_from(j, end);
     }
 };
 

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     // The parts that hold the beginnings of the job's first and last tile.  Part c
     // is the one to work if it is the second of several.
     const int first = range_of(h.job_start, h.x_total, P);
-    const int last = range_of(h.job_start + tile_begin(a, j, j.nt - 1), h.x_total, P);
+    const int last = range_of(h.job_start + tile_begin(j, j.nt - 1), h.x_total, P);
     if (c != first + 1 || last == first) return;
     const int n = last - first + 1;
     auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(first + i) + (i == 0); };   // see Walk::slot

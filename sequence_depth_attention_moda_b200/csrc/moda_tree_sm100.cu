@@ -35,8 +35,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include <type_traits>
-
 #include "moda_tree.cuh"
 
 namespace moda {
@@ -386,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             __syncwarp();
             if (!more) break;
             r.segment(a, sg);
+            // table entries two tiles ahead: under load a read takes as long as a tile
+            int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
             for (int s = r.first; s <= r.last; ++s) {
                 if (r.used(s) > 0 && !wait_all(L::kQFree + s, r.used(s) - 1)) {
                     ok = false;
@@ -399,8 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 }
             }
             if (!ok) break;
-            // table entries two tiles ahead: under load a read takes as long as a tile
-            int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
             for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
                 const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
                 e0 = e1;
@@ -538,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
             const int n_tok0 = sub_tokens(a, sg, 0), n_tok1 = r.two ? sub_tokens(a, sg, 1) : n_tok0;
             // One block: slot s, tile i; `masks`: some key of the tile is hidden from some row.
             // `clean`: the tile's values are looked over here (a tile's first block does).
-            auto block = [&](auto masks, int i, int s, int n_tok, float& m, float& l, int& prev, bool clean) -> bool {
-                constexpr bool kMasks = decltype(masks)::value;
+            // (One instance, in one loop: short jobs pay for every line of code they touch.)
+            auto block = [&](bool masks, int i, int s, int n_tok, float& m, float& l, int& prev, bool clean) -> bool {
                 const int sb = r.b % L::kNS;
                 if (!wait_all(L::kSFull + sb, r.b / L::kNS)) return false;
                 tc_fence_after();
@@ -550,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     const bool real = t_off < n_tok && t_off < a.Tq;
                     uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;   // of this thread's 64 columns
                     bool blind = false;               // none of the warp's tokens is in this depth tile
-                    if constexpr (kMasks) {
+                    if (masks) {
                         const bool dep = i >= sg.nseq;
                         if (real) {
                             const int c = half * 64;
@@ -583,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                         tmem_ld16x2_32<64>(s_addr + 32, x + 32);
                         tmem_wait_ld();
                         reg_fence<64>(x);
-                        if constexpr (kMasks) {
+                        if (masks) {
 #pragma unroll
                             for (int e = 0; e < 64; ++e)
                                 if (!((e < 32 ? vis0 : vis1) >> (e & 31) & 1)) x[e] = __float_as_uint(-INFINITY);
@@ -642,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     tmem_st16x2_32<32>(s_addr, pk);
                     tmem_wait_st();
                 }
-                if constexpr (kMasks) {
+                if (masks) {
                     // S of this tile is done, so P V of tile j - kVS is, and the stage's phase is this tile's
                     if (clean) {
                         const int st = r.j % L::kVS;
@@ -661,23 +659,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 prev = r.b++;
                 return true;
             };
-            int i = sg.i0;
-            const int open = min(sg.i1, sg.r.held / kTile);       // tiles of held keys alone
-            for (; ok && i < open; ++i, ++r.j) {
-                if (r.first == 0) ok = block(std::false_type{}, i, 0, n_tok0, m0, l0, prev0, false);
-                if (NQ == 2 && ok && r.last == 1) ok = block(std::false_type{}, i, 1, n_tok1, m1, l1, prev1, false);
-            }
-            for (; ok && i < sg.i1; ++i, ++r.j) {
-                bool clean = true;
+            const int open = sg.r.held / kTile;       // tiles of held keys alone come first
+            for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
+                const bool masks = i >= open;
+                bool clean = masks;
 #pragma unroll 1
                 for (int s = r.first; ok && s <= r.last; ++s) {
-                    if (!r.takes(sg, i, s)) continue;
-                    float m = s ? m1 : m0, l = s ? l1 : l0;
-                    int prev = s ? prev1 : prev0;
-                    ok = block(std::true_type{}, i, s, s ? n_tok1 : n_tok0, m, l, prev, clean);
+                    if (masks && !r.takes(sg, i, s)) continue;
+                    if (NQ == 1) {
+                        ok = block(masks, i, 0, n_tok0, m0, l0, prev0, clean);
+                    } else {
+                        float m = s ? m1 : m0, l = s ? l1 : l0;
+                        int prev = s ? prev1 : prev0;
+                        ok = block(masks, i, s, s ? n_tok1 : n_tok0, m, l, prev, clean);
+                        if (s) m1 = m, l1 = l, prev1 = prev;
+                        else m0 = m, l0 = l, prev0 = prev;
+                    }
                     clean = false;
-                    if (s) m1 = m, l1 = l, prev1 = prev;
-                    else m0 = m, l0 = l, prev0 = prev;
                 }
             }
             // ------------------------------------------------ end of segment --
