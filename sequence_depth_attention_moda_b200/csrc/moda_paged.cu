@@ -549,7 +549,7 @@ TreePlan tree_plan(const Paged& p) {
     t.rec_rows = rows < static_cast<long long>(t.Tg) * p.G ? static_cast<int>(rows) : t.Tg * p.G;
     t.off_ml = round256(sizeof(tree::CtaHeader) * t.n_cta);
     t.off_po = t.off_ml + round256(sizeof(float2) * 2 * t.n_cta * t.rec_rows);
-    t.bytes = t.off_po + round256(sizeof(float) * 2 * t.n_cta * t.rec_rows * p.d);
+    t.bytes = 256 + t.off_po + round256(sizeof(float) * 2 * t.n_cta * t.rec_rows * p.d);
     return t;
 }
 
@@ -687,7 +687,9 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         a.q = q; a.kc = k_cache; a.vc = v_cache; a.kd = Kd; a.vd = Vd;
         a.table = block_table; a.held = held_len; a.cu = cu_new; a.mask = mask;
         a.o = o; a.lse = lse;
-        unsigned char* base = static_cast<unsigned char*>(ws);
+        // (whole 256-byte lines of a workspace that need only be 16-byte aligned)
+        unsigned char* base =
+            reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
         a.hdr = reinterpret_cast<tree::CtaHeader*>(base);
         a.ml = reinterpret_cast<float2*>(base + t.off_ml);
         a.po = reinterpret_cast<float*>(base + t.off_po);

@@ -474,6 +474,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
+// 32 bytes to a 32-byte aligned global address: a whole sector a thread.
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // acc + 0 * v for two bf16: NaN once an element was an infinity or a NaN.
 __device__ __forceinline__ uint32_t not_finite_acc(uint32_t v, uint32_t acc) {
     uint32_t r;

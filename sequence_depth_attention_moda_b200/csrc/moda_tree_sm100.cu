@@ -98,6 +98,7 @@ struct SmArgs {
     TreeArgs t;
     TmaMap tq, tk, tv, tkd, tvd;
     int box_rows;        // rows of a cache box: min(page, 128)
+    int wide;            // o is 32-byte aligned: rows are stored by whole sectors
 };
 
 // What the MMA and softmax roles derive alike while they go through the CTA's tiles.
@@ -660,6 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 return true;
             };
             const int open = sg.r.held / kTile;       // tiles of held keys alone come first
+            // the mask rows are wanted only then, and from L1
+            if (a.mask && row0 + (lane & 15) < min(sg.ntok, a.Tg) * a.G) {
+                const uint32_t* m = a.mask + static_cast<size_t>(sg.r.cu0 + sg.tok0 + t_off) * a.words;
+                for (int x = half * 32; x < a.words; x += 64) prefetch_l1(m + x);
+            }
             for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
                 const bool masks = i >= open;
                 bool clean = masks;
@@ -711,22 +717,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 if (whole) {
                     const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + orow * D;
-                    uint4* dst = reinterpret_cast<uint4*>(out + half * (D / 2));
+                    __nv_bfloat16* dst = out + half * (D / 2);
 #pragma unroll
-                    for (int c = 0; c < D / 2; c += 8) {
-                        float v[8];
+                    for (int c = 0; c < D / 2; c += 16) {
+                        uint32_t v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[c + e]) * inv;
-                        dst[c / 8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                pack_bf16(v[6], v[7]));
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = pack_bf16(__uint_as_float(o[c + 2 * e]) * inv, __uint_as_float(o[c + 2 * e + 1]) * inv);
+                        if (g.wide) {
+                            store32(dst + c, v);
+                        } else {
+                            *reinterpret_cast<uint4*>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                        }
                     }
                     if (poison) add_not_finite<__nv_bfloat16, D>(a, sg.r, sg.b, sg.hk, token, out, half * (D / 2), 1, D / 2);
                     if (half == 0) a.lse[orow] = row_lse(m, lt);
                 } else {
                     if (some) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.po + rec * D + half * (D / 2));
+                        float* dst = a.po + rec * D + half * (D / 2);
 #pragma unroll
-                        for (int c = 0; c < D / 2; c += 4) dst[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        for (int c = 0; c < D / 2; c += 8) store32(dst + c, o + c);
                     }
                     // a slot without a block here (only depth tiles of the other one): an empty record
                     if (half == 0) a.ml[rec] = make_float2(m, poison ? -lt : lt);
@@ -749,6 +760,7 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
     SmArgs g;
     g.t = a;
     g.box_rows = p.page < kTile ? p.page : kTile;
+    g.wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     cudaError_t e;
     // A query tile: Tq tokens of the group's G heads, rows token * G + head.
     if ((e = make_tma_3d_bf16(&g.tq, a.q, D, p.Hq, p.N, p.G, t.Tq)) != cudaSuccess) return e;
