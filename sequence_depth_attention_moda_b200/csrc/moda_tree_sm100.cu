@@ -208,7 +208,7 @@ __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int sla
 // which are masked for some query row.  True if it found any.  A call of its
 // own, so that its registers are not the tile loop's.
 template <int D>
-__device__ __noinline__ bool clean_values(unsigned char* stage, int r0, int rows, int from, int pitch, int used) {
+__device__ __forceinline__ bool clean_values(unsigned char* stage, int r0, int rows, int from, int pitch, int used) {
     const int lane = threadIdx.x & 31;
     if (r0 >= rows || r0 + 16 <= from) return false;
     uint4* p = reinterpret_cast<uint4*>(stage) + r0 * 8 + lane;      // row r0 + 4u + lane/8, chunk lane%8 of a slab
@@ -269,7 +269,7 @@ __device__ __noinline__ bool clean_values(unsigned char* stage, int r0, int rows
 
 // mask_visible of 64 keys.  (A call, like clean_values; its arguments are values,
 // since a reference to the kernel's parameters is read through global memory.)
-__device__ __noinline__ uint2 mask_visible64(const uint32_t* row, int words, int n, int rel) {
+__device__ __forceinline__ uint2 mask_visible64(const uint32_t* row, int words, int n, int rel) {
     return make_uint2(mask_visible(row, words, n, rel), mask_visible(row, words, n, rel + 32));
 }
 
