@@ -530,9 +530,15 @@ TreePlan tree_plan(const Paged& p) {
         t.rows = t.KT = 128;
         t.Tq = t.rows / p.G;
         // Two row tiles a job read the keys once for 256 rows, but leave two score
-        // buffers instead of three: for requests that fill one tile on average
-        // the one-tile kernel is faster (csrc/moda_tree_sm100.cu has the figures).
-        t.tiles = per > t.Tq ? 2 : 1;
+        // buffers instead of three, and a job's blocks run one after the other on one
+        // SM.  Where requests fill more than one tile and the cache (as far as the
+        // shape tells) is several times L2, the bytes win: n = 64, G = 4, d = 128, 8
+        // heads, 8 requests: T = 32768 321 us against 368, T = 12288 143 against 151,
+        // T = 8192 108 against 103, T = 4096 75 against 66.  With d = 64 a tile's bytes
+        // are half and its exponentials the same: T = 32768 272 against 257.
+        const double pages = double(p.B) * p.max_pages < p.n_pages ? double(p.B) * p.max_pages : p.n_pages;
+        const double cache = pages * p.page * p.Hk * p.d * 2 * p.elem_bytes;
+        t.tiles = per > t.Tq && p.d == 128 && cache > 320e6 ? 2 : 1;
         t.Lp = (Lw + 7) / 8 * 8;       // a token's depth rows begin on a swizzle atom
         t.n_cta = device_sm_count();
     } else {

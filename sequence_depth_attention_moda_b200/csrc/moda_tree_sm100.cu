@@ -11,9 +11,10 @@
 // tiles, which it streams through a K ring and a V ring.  A job has one or two
 // query tiles of 128 rows; a block is one key tile against one query tile, and
 // a sequence tile is loaded once for both of a job's query tiles (two blocks),
-// a depth tile holds one query tile's tokens (one block).  Jobs of one query
-// tile use the two query slots (shared memory) and O accumulators (TMEM) in
-// turn, so a job's products start while the one before is written out.
+// a depth tile holds one query tile's tokens (one block).  Two instances: jobs
+// of one query tile (NQ = 1), and of up to two, where those of one use the two
+// query slots (shared memory) and O accumulators (TMEM) in turn.  tree_plan
+// chooses and has the figures.
 //
 // Warps: 0 TMA producer (Q, K; a lane a page or a token, so pages as small
 // as 8 rows cost one issue each); 1 TMA producer of V; 2 issues S = Q K^T, up to the number of S buffers ahead; 3 issues O += P V; 4..11
@@ -22,8 +23,8 @@
 // 2^8 (exact: any reference gives the same quotient), P in bf16 over the score
 // columns.  Warps without a real row,
 // and in depth tiles those whose tokens are not in the tile, skip the work.
-// TMEM columns: S buffers from 0 (two for d = 128, three for d = 64), then two
-// O accumulators of d.
+// TMEM columns: S buffers from 0 (three, or two where jobs may have two query
+// tiles), then an O accumulator of d for each slot.
 //
 // A tile that ends a request's keys leaves rows of the V stage unwritten (pages
 // behind the last key are not loaded) or with what the page held; P is 0 there,
@@ -72,9 +73,9 @@ struct Lay {
     static constexpr int kSlabs = D / 64;
     static constexpr uint32_t kTileBytes = kSlabs * kSlab;
     // all of shared memory: V stages are held until P V is done, K stages only until S is
-    static constexpr int kKS = D == 128 ? (NQ == 1 ? 3 : 2) : (NQ == 1 ? 6 : 5);
-    static constexpr int kVS = D == 128 ? 3 : (NQ == 1 ? 7 : 6);
-    static constexpr int kNS = D == 128 && NQ == 2 ? 2 : 3;  // S buffers
+    static constexpr int kKS = D == 64 ? 6 : (NQ == 1 ? 3 : 2);
+    static constexpr int kVS = D == 64 ? 7 : 3;
+    static constexpr int kNS = NQ == 2 ? 2 : 3;             // S buffers
     static constexpr uint32_t kColO = kNS * 128;            // O of slot s: + s * D
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = NQ * kTileBytes;
@@ -797,8 +798,8 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
 }  // namespace
 
 cudaError_t launch_tree_sm100(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
-    if (p.d == 128) return t.tiles == 1 ? launch_d<128, 1>(p, t, a, s) : launch_d<128, 2>(p, t, a, s);
-    return t.tiles == 1 ? launch_d<64, 1>(p, t, a, s) : launch_d<64, 2>(p, t, a, s);
+    if (p.d == 64) return launch_d<64, 1>(p, t, a, s);
+    return t.tiles == 1 ? launch_d<128, 1>(p, t, a, s) : launch_d<128, 2>(p, t, a, s);
 }
 
 }  // namespace moda

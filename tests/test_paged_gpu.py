@@ -261,6 +261,44 @@ def test_tree(c):
     check_tree(c, x, see, o, lse)
 
 
+# bf16 jobs of two row tiles run when requests fill more than one and the cache is
+# several times L2: the same cases with a cache (and a table) that large
+TWO_TILES = [
+    Tree(held=(300, 12), new=(33, 65), Hq=16, Hk=2, L=8, page=8),      # G = 8: 16 tokens a row tile
+    Tree(held=(2000,), new=(200,), chain=True, L=2, Hq=4, Hk=1),
+    Tree(held=(0, 1), new=(150, 90), chain=True, L=0, page=8),
+    Tree(held=(513, 4, 700), new=(64, 1, 40), Hq=32, Hk=8, L=16, window=9),
+    Tree(held=(200, 50), new=(70, 33), L=130),
+    Tree(held=tuple(range(0, 2000, 97)), new=tuple(20 + 3 * k for k in range(21)), Hq=8, Hk=2, L=5, pad=3),
+    Tree(held=(3000, 10), new=(128, 200), Hq=2, Hk=2, page=1024, L=1),
+]
+
+
+def in_large_cache(y, sh, c):
+    """The case in a cache of 360 MB of NaN and a table with as many columns."""
+    n_big = 180_000_000 // (c.Hk * c.page * c.d * 2)
+    for k in ("kc", "vc"):
+        big = torch.full((n_big, *y[k].shape[1:]), float("nan"), dtype=y[k].dtype, device=DEV)
+        big[: sh.n_pages] = y[k]
+        y[k] = big
+    cols = -(-n_big // sh.B)
+    table = torch.full((sh.B, cols), 1 << 30, dtype=torch.int32, device=DEV)
+    table[:, : sh.max_pages] = y["table"]
+    y["table"] = table
+    sh.n_pages, sh.max_pages = n_big, cols
+    return y
+
+
+@pytest.mark.parametrize("c", TWO_TILES, ids=str)
+def test_tree_two_row_tiles(c):
+    x, see, sh = make_tree(c)
+    small = moda.moda_tree_decode_workspace_size(sh)
+    y = in_large_cache(to_device(x), sh, c)
+    assert moda.moda_tree_decode_workspace_size(sh) > small       # records of 256 rows
+    o, lse = run_tree(y, sh)
+    check_tree(c, x, see, o, lse)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("held,L,n", [(0, 0, 40), (5, 0, 40), (0, 3, 9), (200, 2, 70)])
 def test_tree_any_mask(dtype, held, L, n):
@@ -298,6 +336,17 @@ def test_tree_not_finite_where_masked(dtype):
     ref_finite = torch.isfinite(o[:29].float())
     assert not bool(ref_finite.all()) and bool(ref_finite.any())
     # rows with NaN scores are NaN in both; the others are compared
+    check_rows_not_finite(c, x, see, o, lse)
+
+
+def test_tree_not_finite_two_row_tiles():
+    c = Tree(held=(150, 20), new=(70, 40), L=4)
+    x, see, sh = make_tree(c)
+    for b, j, v in ((0, 7, float("inf")), (0, 40, float("nan")), (1, 33, float("-inf"))):
+        key = c.held[b] + j
+        x["vc"][int(x["table"][b][key // c.page]), :, key % c.page, 3] = v
+    x["Vd"][50, 1, 2, 10] = -float("inf")
+    o, lse = run_tree(in_large_cache(to_device(x), sh, c), sh)
     check_rows_not_finite(c, x, see, o, lse)
 
 
