@@ -542,11 +542,12 @@ TreePlan tree_plan(const Paged& p) {
         t.Lp = (Lw + 7) / 8 * 8;       // a token's depth rows begin on a swizzle atom
         t.n_cta = device_sm_count();
     } else {
-        t.KT = 64;
-        t.rows = p.G <= 16 && static_cast<long long>(per) * p.G <= 16 ? 16 : 64;
+        t.KT = 32;
+        const long long rows = static_cast<long long>(per) * p.G;     // of a request and KV head
+        t.rows = p.G <= 4 && rows <= 4 ? 4 : (p.G <= 16 && rows <= 16 ? 16 : 64);
         t.Tq = t.rows / p.G;
         t.Lp = Lw;
-        t.n_cta = device_sm_count() * (t.rows == 64 && p.d == 128 ? 1 : 2);
+        t.n_cta = 2 * device_sm_count();
     }
     t.Tg = t.Tq * t.tiles;
     t.dtok = Lw <= t.KT ? t.KT / t.Lp : 1;

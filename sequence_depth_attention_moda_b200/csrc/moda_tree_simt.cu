@@ -9,13 +9,23 @@
 // by the online form: a running maximum m and sum l, o rescaled by
 // 2^(m_old - m_new) when the maximum grows.  Everything in fp32.
 //
-// CTA: 256 threads, R query rows, tiles of 64 keys in shared memory.  A thread
-// computes 4 rows x 4 keys of S and 4 rows x D/16 columns of O; with R < 64 the
-// 256 threads exceed the 4x4 blocks, and DS = 64/R adjacent lanes split the
-// head dimension of S and the keys of P V, so all of them have work (shuffles
-// join the parts).  R = 16 is taken when the requests' rows fit in it on
-// average (G * tokens <= 16): a 64-row tile would do four times the work on
-// rows that are not there.
+// CTA: 256 threads, R query rows, tiles of 32 keys; two CTAs an SM.  Key and value
+// rows come by cp.async, kStages tiles ahead (a row that is not there is filled
+// with zeros), so the loads of a tile run under the arithmetic of those before.
+// A thread computes 4 rows x 4 keys of S and 4 rows x D/8 columns of O; DS = 128/R
+// lanes of a warp share such a block and split the head dimension of S and the
+// keys of P V, so that all threads have work whatever R is (the parts of S are
+// joined by halving exchanges, those of O once a job).  R = 4, 16 or 64, the least
+// that holds a request's rows on average: padded rows cost as much arithmetic as
+// real ones.  Shared memory rows are padded by 16 bytes, and the lanes are laid out
+// so that the eight of a quarter warp read different banks (with the lanes that
+// share a block always adjacent, R = 64 took 680 us where it now takes 533).
+//
+// Measured (8 requests, 32 query heads over 8, d 128, 8192 keys each): 1 token
+// 146 us (R = 4; keys and values of 0.54 GB at 3.7 TB/s), 4 tokens 233 (R = 16),
+// 16 tokens 533 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
+// reads 8 vectors for 64 multiply-adds, and larger blocks do not fit the registers of
+// two CTAs an SM).  One tile in flight and plain loads: 359, 363 and 743 us.
 #include "moda_tree.cuh"
 
 namespace moda {
@@ -25,189 +35,266 @@ using namespace tree;
 using ptx::ex2;
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 64;
+constexpr int kKeys = 32;
 
 template <int D, int R>
 struct Lay {
-    static constexpr int kQ = 0;                              // float [R][D+4]
-    static constexpr int kK = kQ + R * (D + 4) * 4;           // float [64][D+4]
-    static constexpr int kV = kK + kKeys * (D + 4) * 4;       // float [64][D]
-    static constexpr int kP = kV + kKeys * D * 4;             // float [R][64+4]
-    static constexpr int kRow = kP + R * (kKeys + 4) * 4;     // long long [64]: element offset, -1: no row
-    static constexpr int kStat = kRow + kKeys * 8;            // float [3][R]: alpha, m, l
+    static constexpr int kPitch = D + 4;                       // floats of a row
+    static constexpr int kStages = D == 128 ? (R == 64 ? 2 : 3) : (R == 64 ? 4 : 5);
+    static constexpr int kTile = kKeys * kPitch * 4;           // bytes of a K (or V) tile
+    static constexpr int kQ = 0;                               // float [R][kPitch]
+    static constexpr int kKV = kQ + R * kPitch * 4;            // [kStages][K, V][32][kPitch]
+    static constexpr int kP = kKV + kStages * 2 * kTile;       // float [R][32+4]
+    static constexpr int kStat = kP + R * (kKeys + 4) * 4;     // float [3][R]: alpha, m, l
     static constexpr int kStart = (kStat + 3 * R * 4 + 15) / 16 * 16;
-    static constexpr int kBytes = kStart + static_cast<int>(sizeof(Start)) + 16;
+    static constexpr int kWalk = kStart + (static_cast<int>(sizeof(Start)) + 15) / 16 * 16;
+    static constexpr int kBytes = kWalk + static_cast<int>(sizeof(Walk)) + 16;
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// Sums v[0..N) over the DS lanes of a group (lane % DS = ds); lane ds ends with
+// the N/DS sums v[ds * N/DS ..] in place (DS <= N), or, for more lanes than
+// values, each with the sum it shares with DS/N - 1 others.  Adjacent parts are
+// kStep lanes apart.
+template <int N, int DS, int kStep>
+__device__ __forceinline__ void group_sum(float* v, int ds) {
+    if constexpr (DS > 1) {
+        constexpr int H = DS / 2;
+        if constexpr (N > 1) {
+            const bool up = ds & H;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float give = up ? v[i] : v[i + N / 2], keep = up ? v[i + N / 2] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, H * kStep);
+            }
+            group_sum<N / 2, H, kStep>(v, ds & (H - 1));
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], H * kStep);
+            group_sum<1, H, kStep>(v, ds & (H - 1));
+        }
+    }
+}
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
     using L = Lay<D, R>;
-    constexpr int DS = 64 / R;            // lanes sharing a 4x4 block
+    constexpr int DS = 128 / R;           // lanes sharing a block
     constexpr int TPR = kThreads / R;     // softmax threads per row
+    constexpr int KPT = kKeys / TPR > 0 ? kKeys / TPR : 1;    // keys each has
+    constexpr int NC = D / 32;            // float4 columns of O per thread
+    constexpr int CH = D / 4;             // 16-byte chunks of a row
+    constexpr int CPT = kKeys * CH / kThreads;    // chunks of a K (and V) tile a thread copies
     extern __shared__ __align__(16) unsigned char smem[];
     float* sq = reinterpret_cast<float*>(smem + L::kQ);
-    float* sk = reinterpret_cast<float*>(smem + L::kK);
-    float* sv = reinterpret_cast<float*>(smem + L::kV);
+    float* skv = reinterpret_cast<float*>(smem + L::kKV);
     float* sp = reinterpret_cast<float*>(smem + L::kP);
-    long long* srow = reinterpret_cast<long long*>(smem + L::kRow);
     float* salpha = reinterpret_cast<float*>(smem + L::kStat);
     float* sm = salpha + R;
     float* sl = sm + R;
     Start* st = reinterpret_cast<Start*>(smem + L::kStart);
-    int* spoison = reinterpret_cast<int*>(st + 1);
+    // the walk over the jobs, advanced by thread 0: in registers it would crowd out the accumulators
+    Walk& w = *reinterpret_cast<Walk*>(smem + L::kWalk);
+    int* spoison = reinterpret_cast<int*>(&w + 1);
+    int* smore = spoison + 1;
 
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     schedule(a, st);
     const int tid = threadIdx.x;
-    const int ds = tid % DS;
-    const int cg = (tid / DS) % 16;       // keys cg + 16c of S, columns 4cg + 64j of O
-    const int rg = tid / DS / 16;         // rows 4rg .. 4rg+3
+    // A quarter warp reads eight 16-byte pieces at a time, free of bank conflicts if
+    // it is eight parts of a block or eight blocks' same part.
+    constexpr int kStep = DS < 8 ? 8 : 1;
+    const int ds = tid / kStep % DS;
+    const int cg = kStep == 1 ? tid / DS % 8 : tid % 8;       // keys cg + 8c of S, columns 4cg + 32j of O
+    const int rg = tid / DS / 8;          // rows 4rg .. 4rg+3
     const int page = 1 << a.page_shift;
 
-    Walk w;
-    for (bool more = w.begin(a, *st); more; more = w.next(a)) {
+    for (bool first = true;; first = false) {
+        __syncthreads();                  // the previous job is done with shared memory
+        if (tid == 0) {
+            *smore = first ? w.begin(a, *st) : w.next(a);
+            *spoison = 0;
+        }
+        __syncthreads();
+        if (!*smore) break;
         const Job& j = w.j;
         const int rows = j.ntok * a.G;
-        __syncthreads();                  // the previous job is done with shared memory
-        if (tid == 0) *spoison = 0;
-        for (int i = tid; i < R * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = i % (D / 4) * 4;
+        // This thread's chunks of a tile: column tid % CH of rows tid / CH, + kThreads / CH, ...
+        // Table entries of the rows, asked for a tile before they are used.
+        int entry[CPT];
+        auto ask = [&](int t) {
+#pragma unroll
+            for (int u = 0; u < CPT; ++u) {
+                const int key = t * kKeys + tid / CH + u * (kThreads / CH);
+                entry[u] = t < min(w.i1, j.nseq) && key < j.r.held + j.r.n ? table_entry(a, j.b, key) : -1;
+            }
+        };
+        auto load = [&](int t, int stage) {
+            const bool seq = t < j.nseq;
+            const float* kb = static_cast<const float*>(seq ? a.kc : a.kd);
+            const float* vb = static_cast<const float*>(seq ? a.vc : a.vd);
+            float* dst = skv + stage * (2 * L::kTile / 4);
+#pragma unroll
+            for (int u = 0; u < CPT; ++u) {
+                const int r = tid / CH + u * (kThreads / CH), c = tid % CH * 4;
+                long long off = -1;       // the row's first element, -1: not there
+                if (seq) {
+                    const int key = t * kKeys + r;
+                    if (key < j.r.held + j.r.n) {
+                        const int p = checked_page(a, entry[u]);
+                        if (p >= 0) off = ((static_cast<long long>(p) * a.Hk + j.hk) * page + (key & (page - 1))) * D;
+                    }
+                } else {
+                    const int dt = t - j.nseq;
+                    int tok, d;
+                    if (a.Lw <= a.KT) {
+                        const int at = r / a.Lp;
+                        tok = at < a.dtok ? dt * a.dtok + at : j.ntok;
+                        d = r - at * a.Lp;
+                    } else {
+                        tok = dt / a.dsplit;
+                        d = (dt - tok * a.dsplit) * a.KT + r;
+                    }
+                    if (d < a.Lw && tok < j.ntok)
+                        off = ((static_cast<long long>(j.r.cu0 + j.tok0 + tok) * a.Hk + j.hk) * a.L + a.win_lo + d) * D;
+                }
+                const bool there = off >= 0;
+                const long long from = there ? off + c : 0;
+                copy16(dst + r * L::kPitch + c, kb + from, there);
+                copy16(dst + L::kTile / 4 + r * L::kPitch + c, vb + from, there);
+            }
+        };
+        ask(w.i0);
+#pragma unroll 1
+        for (int s = 0; s < L::kStages - 1; ++s) {
+            if (w.i0 + s < w.i1) {
+                load(w.i0 + s, s);
+                ask(w.i0 + s + 1);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        for (int i = tid; i < R * CH; i += kThreads) {
+            const int r = i / CH, c = i % CH * 4;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r < rows) {
                 const size_t row = static_cast<size_t>(j.r.cu0 + j.tok0 + r / a.G) * a.Hq + j.hk * a.G + r % a.G;
-                v = load4(static_cast<const float*>(a.q) + row * D + c);
+                v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row * D + c);
             }
-            *reinterpret_cast<float4*>(&sq[r * (D + 4) + c]) =
+            *reinterpret_cast<float4*>(&sq[r * L::kPitch + c]) =
                 make_float4(v.x * a.scale_log2, v.y * a.scale_log2, v.z * a.scale_log2, v.w * a.scale_log2);
         }
-        float o[4][D / 64][4];
+        float o[4][NC][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) o[r][c][0] = o[r][c][1] = o[r][c][2] = o[r][c][3] = 0.0f;
-        // softmax state of row tid / TPR, the same in its TPR threads
+            for (int c = 0; c < NC; ++c) o[r][c][0] = o[r][c][1] = o[r][c][2] = o[r][c][3] = 0.0f;
+        // softmax state of row tid / TPR, the same in its threads
         const int srw = tid / TPR, sub = tid % TPR;
         float m = -INFINITY, l = 0.0f;
         const int token = j.tok0 + srw / a.G;        // relative to the request
         const bool real = srw < rows;
 
+        int stage = 0;
         for (int t = w.i0; t < w.i1; ++t) {
             const bool dep = t >= j.nseq;
             const int dt = t - j.nseq;
             // rows of V from key row `from` on are masked for some query row
             const int from = dep ? 0 : j.r.held - t * kKeys;
-            __syncthreads();
-            if (tid < kKeys) {
-                long long off = -1;
-                if (!dep) {
-                    const int key = t * kKeys + tid;
-                    if (key < j.r.held + j.r.n) {
-                        const int p = page_of(a, j.b, key);
-                        if (p >= 0)
-                            off = ((static_cast<long long>(p) * a.Hk + j.hk) * page + (key & (page - 1))) * D;
-                    }
-                } else {
-                    int tok, d;
-                    if (a.Lw <= a.KT) {
-                        tok = dt * a.dtok + tid / a.Lp;
-                        d = tid % a.Lp;
-                        if (tid / a.Lp >= a.dtok || d >= a.Lw) tok = j.ntok;
-                    } else {
-                        tok = dt / a.dsplit;
-                        d = dt % a.dsplit * a.KT + tid;
-                        if (d >= a.Lw) tok = j.ntok;
-                    }
-                    if (tok < j.ntok)
-                        off = ((static_cast<long long>(j.r.cu0 + j.tok0 + tok) * a.Hk + j.hk) * a.L + a.win_lo + d) * D;
-                }
-                srow[tid] = off;
-            }
-            __syncthreads();
-            const float* kb = static_cast<const float*>(dep ? a.kd : a.kc);
-            const float* vb = static_cast<const float*>(dep ? a.vd : a.vc);
-#pragma unroll 8
-            for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-                const int r = i / (D / 4), c = i % (D / 4) * 4;
-                const long long off = srow[r];
-                float4 kv = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vv = kv;
-                if (off >= 0) {
-                    kv = load4(kb + off + c);
-                    vv = load4(vb + off + c);
-                }
-                if (r >= from) {
-                    float* e = &vv.x;
+            float* sk = skv + stage * (2 * L::kTile / 4);
+            float* sv = sk + L::kTile / 4;
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 2) : "memory");
+            if (from < kKeys) {           // each thread looks over the chunks it copied
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (!isfinite(e[k])) {
-                            e[k] = 0.0f;
-                            *spoison = 1;
-                        }
+                for (int u = 0; u < CPT; ++u) {
+                    const int r = tid / CH + u * (kThreads / CH), c = tid % CH * 4;
+                    if (r < from) continue;
+                    float4 v = *reinterpret_cast<float4*>(sv + r * L::kPitch + c);
+                    if (isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w)) continue;
+                    v.x = isfinite(v.x) ? v.x : 0.0f;
+                    v.y = isfinite(v.y) ? v.y : 0.0f;
+                    v.z = isfinite(v.z) ? v.z : 0.0f;
+                    v.w = isfinite(v.w) ? v.w : 0.0f;
+                    *reinterpret_cast<float4*>(sv + r * L::kPitch + c) = v;
+                    *spoison = 1;
                 }
-                *reinterpret_cast<float4*>(&sk[r * (D + 4) + c]) = kv;
-                *reinterpret_cast<float4*>(&sv[r * D + c]) = vv;
             }
-            __syncthreads();
+            __syncthreads();              // the tile is there, and the one before done with
+            {
+                const int next = t + L::kStages - 1;
+                if (next < w.i1) {
+                    load(next, stage == 0 ? L::kStages - 1 : stage - 1);
+                    ask(next + 1);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
             // S: 4 rows x 4 keys over this lane's share of the head dimension
-            float s[4][4] = {};
+            float s[16] = {};             // [row][key]
 #pragma unroll 4
             for (int d = ds * 4; d < D; d += 4 * DS) {
-                float4 qv[4], kv[4];
+                float4 qv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    qv[i] = *reinterpret_cast<const float4*>(&sq[(4 * rg + i) * (D + 4) + d]);
-                    kv[i] = *reinterpret_cast<const float4*>(&sk[(cg + 16 * i) * (D + 4) + d]);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[r][c] = fmaf(qv[r].x, kv[c].x, s[r][c]);
-                        s[r][c] = fmaf(qv[r].y, kv[c].y, s[r][c]);
-                        s[r][c] = fmaf(qv[r].z, kv[c].z, s[r][c]);
-                        s[r][c] = fmaf(qv[r].w, kv[c].w, s[r][c]);
-                    }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
+                for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sq[(4 * rg + i) * L::kPitch + d]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    const float4 kv = *reinterpret_cast<const float4*>(&sk[(cg + 8 * c) * L::kPitch + d]);
 #pragma unroll
-                    for (int x = 1; x < DS; x <<= 1) s[r][c] += __shfl_xor_sync(0xffffffffu, s[r][c], x);
-                    if (ds == 0) sp[(4 * rg + r) * (kKeys + 4) + cg + 16 * c] = s[r][c];
+                    for (int r = 0; r < 4; ++r) {
+                        float x = s[4 * r + c];
+                        x = fmaf(qv[r].x, kv.x, x);
+                        x = fmaf(qv[r].y, kv.y, x);
+                        x = fmaf(qv[r].z, kv.z, x);
+                        s[4 * r + c] = fmaf(qv[r].w, kv.w, x);
+                    }
                 }
-            __syncthreads();
-            // online softmax: this row's keys sub, sub + TPR, ...
+            }
+            group_sum<16, DS, kStep>(s, ds);
             {
-                uint32_t vis[2];
+                constexpr int mine = DS <= 16 ? 16 / DS : 1;
+                const int first = DS <= 16 ? ds * mine : ds / (DS / 16);
+                if (DS <= 16 || ds % (DS / 16) == 0) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    vis[h] = !real ? 0u
-                                   : (dep ? dep_visible(a, token - j.tok0, dt, 32 * h)
-                                          : seq_visible(a, j.r, token, t * kKeys + 32 * h));
-                float x[kKeys / TPR], mx = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < kKeys / TPR; ++k) {
-                    const int c = sub + k * TPR;
-                    x[k] = ((c < 32 ? vis[0] : vis[1]) >> (c & 31)) & 1u ? sp[srw * (kKeys + 4) + c] : -INFINITY;
-                    mx = fmaxf(mx, x[k]);
+                    for (int i = 0; i < mine; ++i) {
+                        const int x = first + i;             // row x / 4, key x % 4 of the block
+                        sp[(4 * rg + x / 4) * (kKeys + 4) + cg + 8 * (x % 4)] = s[i];
+                    }
                 }
+            }
+            __syncthreads();
+            // online softmax: this row's keys sub, sub + TPR, ... (a row's spare threads repeat the last keys)
+            {
+                const uint32_t vis = !real ? 0u
+                                           : (dep ? dep_visible(a, token - j.tok0, dt, 0)
+                                                  : seq_visible(a, j.r, token, t * kKeys));
+                float x[KPT], mx = -INFINITY;
+                float* row = &sp[srw * (kKeys + 4)];
 #pragma unroll
-                for (int y = 1; y < TPR; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+                for (int i = 0; i < KPT; ++i) {
+                    const int c = (sub + i * TPR) & (kKeys - 1);
+                    x[i] = vis >> c & 1u ? row[c] : -INFINITY;
+                    mx = fmaxf(mx, x[i]);
+                }
+                constexpr int W = TPR < 32 ? TPR : 32;       // the row's threads within a warp
+#pragma unroll
+                for (int y = 1; y < W; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
                 const float mn = fmaxf(m, mx);
                 const float ref = mn == -INFINITY ? 0.0f : mn;       // a row that saw no key yet
                 const float alpha = m == -INFINITY ? 1.0f : ex2(m - mn);   // its o and l are 0
                 float ps = 0.0f;
+                if (TPR > kKeys) __syncthreads();            // two warps read the row
 #pragma unroll
-                for (int k = 0; k < kKeys / TPR; ++k) {
-                    const float p = ex2(x[k] - ref);
+                for (int i = 0; i < KPT; ++i) {
+                    const float p = ex2(x[i] - ref);
                     ps += p;
-                    sp[srw * (kKeys + 4) + sub + k * TPR] = p;
+                    row[(sub + i * TPR) & (kKeys - 1)] = p;
                 }
 #pragma unroll
-                for (int y = 1; y < TPR; y <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, y);
+                for (int y = 1; y < W; y <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, y);
                 l = fmaf(l, alpha, ps);
                 m = mn;
                 if (sub == 0) salpha[srw] = alpha;
@@ -218,29 +305,30 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
             for (int r = 0; r < 4; ++r) {
                 const float al = salpha[4 * rg + r];
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
+                for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[r][c][e] *= al;
             }
-#pragma unroll 4
+#pragma unroll 2
             for (int k = ds; k < kKeys; k += DS) {
-                float4 vv[D / 64];
+                float p[4];
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    vv[c] = *reinterpret_cast<const float4*>(&sv[k * D + 4 * cg + 64 * c]);
+                for (int r = 0; r < 4; ++r) p[r] = sp[(4 * rg + r) * (kKeys + 4) + k];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float p = sp[(4 * rg + r) * (kKeys + 4) + k];
+                for (int c = 0; c < NC; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(&sv[k * L::kPitch + 4 * cg + 32 * c]);
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        o[r][c][0] = fmaf(p, vv[c].x, o[r][c][0]);
-                        o[r][c][1] = fmaf(p, vv[c].y, o[r][c][1]);
-                        o[r][c][2] = fmaf(p, vv[c].z, o[r][c][2]);
-                        o[r][c][3] = fmaf(p, vv[c].w, o[r][c][3]);
+                    for (int r = 0; r < 4; ++r) {
+                        o[r][c][0] = fmaf(p[r], v.x, o[r][c][0]);
+                        o[r][c][1] = fmaf(p[r], v.y, o[r][c][1]);
+                        o[r][c][2] = fmaf(p[r], v.z, o[r][c][2]);
+                        o[r][c][3] = fmaf(p[r], v.w, o[r][c][3]);
                     }
                 }
             }
+            if (++stage == L::kStages) stage = 0;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (sub == 0) {
             sm[srw] = m;
             sl[srw] = l;
@@ -250,25 +338,27 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
         const bool whole = w.whole();
         const size_t slot = w.slot();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 4 * rg + r;
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int x = 1; x < DS; x <<= 1)
-                        o[r][c][e] += __shfl_xor_sync(0xffffffffu, o[r][c][e], x);
+                    for (int y = 1; y < DS; y <<= 1)
+                        o[r][c][e] += __shfl_xor_sync(0xffffffffu, o[r][c][e], y * kStep);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 4 * rg + r;
             if (row >= rows || ds != 0) continue;
             const float lr = sl[row], mr = sm[row];
             if (whole) {
                 const int tk = j.tok0 + row / a.G;
                 const size_t orow = static_cast<size_t>(j.r.cu0 + tk) * a.Hq + j.hk * a.G + row % a.G;
                 const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
+                float* out = static_cast<float*>(a.o) + orow * D;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const int col = 4 * cg + 64 * c;
-                    float* out = static_cast<float*>(a.o) + orow * D;
+                for (int c = 0; c < NC; ++c) {
+                    const int col = 4 * cg + 32 * c;
                     *reinterpret_cast<float4*>(out + col) =
                         make_float4(o[r][c][0] * inv, o[r][c][1] * inv, o[r][c][2] * inv, o[r][c][3] * inv);
                     if (poison) add_not_finite<float, D>(a, j.r, j.b, j.hk, tk, out, col, 1, 4);
@@ -277,8 +367,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_consta
             } else {
                 const size_t rec = slot * a.rec_rows + row;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    *reinterpret_cast<float4*>(a.po + rec * D + 4 * cg + 64 * c) =
+                for (int c = 0; c < NC; ++c)
+                    *reinterpret_cast<float4*>(a.po + rec * D + 4 * cg + 32 * c) =
                         make_float4(o[r][c][0], o[r][c][1], o[r][c][2], o[r][c][3]);
                 if (cg == 0) a.ml[rec] = make_float2(mr, poison ? -lr : lr);
             }
@@ -302,6 +392,12 @@ cudaError_t launch_r(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, tree_simt_kernel<D, R>, a);
+}
+
+template <int D>
+cudaError_t launch_d(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
+    if (t.rows == 4) return launch_r<D, 4>(t, a, s);
+    return t.rows == 16 ? launch_r<D, 16>(t, a, s) : launch_r<D, 64>(t, a, s);
 }
 
 // Merges the records of a job that range ends cut: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
@@ -398,8 +494,7 @@ cudaError_t launch_combine(const TreePlan& t, const TreeArgs& a, cudaStream_t s)
 }  // namespace
 
 cudaError_t launch_tree_simt(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
-    if (p.d == 128) return t.rows == 16 ? launch_r<128, 16>(t, a, s) : launch_r<128, 64>(t, a, s);
-    return t.rows == 16 ? launch_r<64, 16>(t, a, s) : launch_r<64, 64>(t, a, s);
+    return p.d == 128 ? launch_d<128>(t, a, s) : launch_d<64>(t, a, s);
 }
 
 cudaError_t launch_tree_combine(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
