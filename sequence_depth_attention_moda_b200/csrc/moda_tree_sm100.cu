@@ -17,12 +17,13 @@
 // chooses and has the figures.
 //
 // Warps: 0 TMA producer (Q, K; a lane a page or a token, so pages as small
-// as 8 rows cost one issue each); 1 TMA producer of V; 2 issues S = Q K^T, up to the number of S buffers ahead; 3 issues O += P V; 4..11
-// softmax, 16 rows a warp and two threads a row (columns [0,64) and [64,128)): O
-// and l are rescaled only when the maximum passes the reference by more than
-// 2^8 (exact: any reference gives the same quotient), P in bf16 over the score
-// columns.  Warps without a real row,
-// and in depth tiles those whose tokens are not in the tile, skip the work.
+// as 8 rows cost one issue each); 1 TMA producer of V; 2 issues S = Q K^T, up to
+// the number of S buffers ahead; 3 issues O += P V; 4..11 softmax, 16 rows a warp
+// and two threads a row (columns [0,64) and [64,128)): O and l are rescaled only
+// when the maximum passes the reference by more than 2^8 (exact: any reference
+// gives the same quotient), P in bf16 over the score columns.  Warps without a
+// real row, and in depth tiles those whose tokens are not in the tile, skip the
+// work.
 // TMEM columns: S buffers from 0 (three, or two where jobs may have two query
 // tiles), then an O accumulator of d for each slot.
 //
@@ -84,7 +85,8 @@ struct Lay {
     // barrier indexes; from kPReady on they take an arrival of each softmax warp
     static constexpr int kQFull = 0, kQFree = NQ, kKFull = 2 * NQ, kKEmpty = kKFull + kKS, kVFull = kKEmpty + kKS,
                          kVEmpty = kVFull + kVS, kSFull = kVEmpty + kVS, kSFree = kSFull + kNS,
-                         kOFull = kSFree + kNS, kSegFull = kOFull + NQ, kPReady = kSegFull + kSegs, kOFree = kPReady + kNS, kNumBars = kOFree + NQ;
+                         kOFull = kSFree + kNS, kSegFull = kOFull + NQ, kPReady = kSegFull + kSegs,
+                         kOFree = kPReady + kNS, kNumBars = kOFree + NQ;
     static constexpr uint32_t kStart = kBar + (kNumBars * 8 + 15) / 16 * 16;
     static constexpr uint32_t kSeg = kStart + (sizeof(Start) + 15) / 16 * 16;
     static constexpr uint32_t kMisc = kSeg + kSegs * sizeof(Seg);       // tmem base, abort flag, marks
@@ -359,167 +361,167 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
     // (two query tiles' statistics); local memory has next to no L1 beside this
     // much shared memory, so a spill in the block loop costs thousands of cycles
     if (warp < 4) {
-    regs_dec<NQ == 1 ? 104 : 88>();
-    if (warp == 0) {
-        // ------------------------------------------------- producer of Q, K --
-        const uint32_t q_bytes = L::kSlabs * 128u * a.Tq * a.G;
-        bool ok = true;
-        Walk w;
-        for (bool more = w.begin(a, *start); ok; more = w.next(a)) {
-            ++k;
-            sg.r = w.j.r;
-            sg.b = w.j.b;
-            sg.hk = w.j.hk;
-            sg.tok0 = w.j.tok0;
-            sg.ntok = w.j.ntok;
-            sg.nseq = w.j.nseq;
-            sg.ndep0 = w.j.ndep0;
-            sg.keys = w.j.r.held + (a.mask ? w.j.r.n : w.j.tok0 + w.j.ntok);
-            sg.i0 = w.i0;
-            sg.i1 = more ? w.i1 : -1;
-            sg.whole = w.whole();
-            sg.slot = w.slot();
+        regs_dec<NQ == 1 ? 104 : 88>();
+        if (warp == 0) {
+            // ------------------------------------------------- producer of Q, K --
+            const uint32_t q_bytes = L::kSlabs * 128u * a.Tq * a.G;
+            bool ok = true;
+            Walk w;
+            for (bool more = w.begin(a, *start); ok; more = w.next(a)) {
+                ++k;
+                sg.r = w.j.r;
+                sg.b = w.j.b;
+                sg.hk = w.j.hk;
+                sg.tok0 = w.j.tok0;
+                sg.ntok = w.j.ntok;
+                sg.nseq = w.j.nseq;
+                sg.ndep0 = w.j.ndep0;
+                sg.keys = w.j.r.held + (a.mask ? w.j.r.n : w.j.tok0 + w.j.ntok);
+                sg.i0 = w.i0;
+                sg.i1 = more ? w.i1 : -1;
+                sg.whole = w.whole();
+                sg.slot = w.slot();
+                if (lane == 0) {
+                    segs[k % kSegs] = sg;
+                    mbar_arrive(&bars[L::kSegFull + k % kSegs]);
+                }
+                __syncwarp();
+                if (!more) break;
+                r.segment(a, sg);
+                // table entries two tiles ahead: under load a read takes as long as a tile
+                int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
+                for (int s = r.first; s <= r.last; ++s) {
+                    if (r.used(s) > 0 && !wait_all(L::kQFree + s, r.used(s) - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars[L::kQFull + s], q_bytes);
+                        for (int x = 0; x < L::kSlabs; ++x)
+                            tma_load_3d(smem + L::kQ + s * L::kTileBytes + x * kSlab, &g.tq, &bars[L::kQFull + s], x * 64,
+                                        sg.hk * a.G, sg.r.cu0 + sg.tok0 + r.sub(s) * a.Tq);
+                    }
+                }
+                if (!ok) break;
+                for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
+                    const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
+                    e0 = e1;
+                    e1 = box_entry(a, g.box_rows, sg, i + 2, lane);
+                    const int st = r.j % L::kKS;
+                    if (r.j >= L::kKS && !wait_all(L::kKEmpty + st, r.j / L::kKS - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    load_tile(x, L::kKFull + st, smem + L::kK + st * L::kTileBytes, &g.tk, &g.tkd);
+                }
+                r.end_segment();
+            }
             if (lane == 0) {
-                segs[k % kSegs] = sg;
-                mbar_arrive(&bars[L::kSegFull + k % kSegs]);
+                for (int s = 0; s < NQ; ++s)
+                    if (r.used(s) > 0) drain(L::kQFull + s, 1, r.used(s));
+                drain(L::kKFull, L::kKS, r.j);
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------- producer of V -----
+            bool ok = true;
+            while (ok && next_seg_all()) {
+                int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
+                for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
+                    const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
+                    e0 = e1;
+                    e1 = box_entry(a, g.box_rows, sg, i + 2, lane);
+                    const int st = r.j % L::kVS;
+                    if (r.j >= L::kVS && !wait_all(L::kVEmpty + st, r.j / L::kVS - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    load_tile(x, L::kVFull + st, smem + L::kV + st * L::kTileBytes, &g.tv, &g.tvd);
+                }
+            }
+            if (lane == 0) drain(L::kVFull, L::kVS, r.j);
+        } else if (warp == 2) {
+            // ------------------------------------------------------ S = Q K^T -----
+            if (elect_one()) {
+                const uint32_t id = idesc_bf16(128, kTile, false, false);
+                const uint64_t qd = desc_kmajor_sw128(smem_u32(smem + L::kQ));
+                const uint64_t kd = desc_kmajor_sw128(smem_u32(smem + L::kK));
+                bool ok = true;
+                while (ok && next_seg_one()) {
+                    r.segment(a, sg);
+                    for (int s = r.first; ok && s <= r.last; ++s) ok = wait(L::kQFull + s, r.used(s));
+                    for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
+                        const int st = r.j % L::kKS;
+                        if (!(ok = wait(L::kKFull + st, r.j / L::kKS))) break;
+                        for (int s = r.first; s <= r.last; ++s) {
+                            if (!r.takes(sg, i, s)) continue;
+                            // the buffer holds P of block b - kNS until its P V is done
+                            const int sb = r.b % L::kNS;
+                            if (r.b >= L::kNS && !(ok = wait(L::kSFree + sb, r.b / L::kNS - 1))) break;
+                            tc_fence_after();
+                            const uint64_t q0 = qd + ((s * L::kTileBytes) >> 4);
+                            const uint64_t k0 = kd + ((st * L::kTileBytes) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+                                umma_ss(tmem + sb * 128, q0 + off, k0 + off, id, kk > 0 ? 1u : 0u);
+                            }
+                            umma_commit(&bars[L::kSFull + sb]);
+                            ++r.b;
+                        }
+                        if (ok) umma_commit(&bars[L::kKEmpty + st]);
+                    }
+                    if (ok)
+                        for (int s = r.first; s <= r.last; ++s) umma_commit(&bars[L::kQFree + s]);
+                    r.end_segment();
+                }
             }
             __syncwarp();
-            if (!more) break;
-            r.segment(a, sg);
-            // table entries two tiles ahead: under load a read takes as long as a tile
-            int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
-            for (int s = r.first; s <= r.last; ++s) {
-                if (r.used(s) > 0 && !wait_all(L::kQFree + s, r.used(s) - 1)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars[L::kQFull + s], q_bytes);
-                    for (int x = 0; x < L::kSlabs; ++x)
-                        tma_load_3d(smem + L::kQ + s * L::kTileBytes + x * kSlab, &g.tq, &bars[L::kQFull + s], x * 64,
-                                    sg.hk * a.G, sg.r.cu0 + sg.tok0 + r.sub(s) * a.Tq);
-                }
-            }
-            if (!ok) break;
-            for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
-                const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
-                e0 = e1;
-                e1 = box_entry(a, g.box_rows, sg, i + 2, lane);
-                const int st = r.j % L::kKS;
-                if (r.j >= L::kKS && !wait_all(L::kKEmpty + st, r.j / L::kKS - 1)) {
-                    ok = false;
-                    break;
-                }
-                load_tile(x, L::kKFull + st, smem + L::kK + st * L::kTileBytes, &g.tk, &g.tkd);
-            }
-            r.end_segment();
-        }
-        if (lane == 0) {
-            for (int s = 0; s < NQ; ++s)
-                if (r.used(s) > 0) drain(L::kQFull + s, 1, r.used(s));
-            drain(L::kKFull, L::kKS, r.j);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------- producer of V -----
-        bool ok = true;
-        while (ok && next_seg_all()) {
-            int e0 = box_entry(a, g.box_rows, sg, sg.i0, lane), e1 = box_entry(a, g.box_rows, sg, sg.i0 + 1, lane);
-            for (int i = sg.i0; i < sg.i1; ++i, ++r.j) {
-                const Box x = tile_box(a, g.box_rows, L::kSlabs, sg, i, e0, lane);
-                e0 = e1;
-                e1 = box_entry(a, g.box_rows, sg, i + 2, lane);
-                const int st = r.j % L::kVS;
-                if (r.j >= L::kVS && !wait_all(L::kVEmpty + st, r.j / L::kVS - 1)) {
-                    ok = false;
-                    break;
-                }
-                load_tile(x, L::kVFull + st, smem + L::kV + st * L::kTileBytes, &g.tv, &g.tvd);
-            }
-        }
-        if (lane == 0) drain(L::kVFull, L::kVS, r.j);
-    } else if (warp == 2) {
-        // ------------------------------------------------------ S = Q K^T -----
-        if (elect_one()) {
-            const uint32_t id = idesc_bf16(128, kTile, false, false);
-            const uint64_t qd = desc_kmajor_sw128(smem_u32(smem + L::kQ));
-            const uint64_t kd = desc_kmajor_sw128(smem_u32(smem + L::kK));
-            bool ok = true;
-            while (ok && next_seg_one()) {
-                r.segment(a, sg);
-                for (int s = r.first; ok && s <= r.last; ++s) ok = wait(L::kQFull + s, r.used(s));
-                for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
-                    const int st = r.j % L::kKS;
-                    if (!(ok = wait(L::kKFull + st, r.j / L::kKS))) break;
-                    for (int s = r.first; s <= r.last; ++s) {
-                        if (!r.takes(sg, i, s)) continue;
-                        // the buffer holds P of block b - kNS until its P V is done
-                        const int sb = r.b % L::kNS;
-                        if (r.b >= L::kNS && !(ok = wait(L::kSFree + sb, r.b / L::kNS - 1))) break;
-                        tc_fence_after();
-                        const uint64_t q0 = qd + ((s * L::kTileBytes) >> 4);
-                        const uint64_t k0 = kd + ((st * L::kTileBytes) >> 4);
+        } else if (warp == 3) {
+            // ------------------------------------------------------ O += P V ------
+            if (elect_one()) {
+                const uint32_t id = idesc_bf16(128, D, false, true);
+                const uint64_t vd = desc_mnmajor_sw128(smem_u32(smem + L::kV), kSlab);
+                bool ok = true;
+                while (ok && next_seg_one()) {
+                    r.segment(a, sg);
+                    // the slots' accumulators must have been read out
+                    for (int s = r.first; ok && s <= r.last; ++s)
+                        if (r.used(s) > 0) ok = wait(L::kOFree + s, r.used(s) - 1);
+                    int begun = 0;                        // slots with a product in this segment (bits)
+                    for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
+                        const int st = r.j % L::kVS;
+                        const int steps = (tile_rows(a, sg, i) + 15) / 16;     // 16 keys each
+                        if (!(ok = wait(L::kVFull + st, r.j / L::kVS))) break;
+                        for (int s = r.first; s <= r.last; ++s) {
+                            if (!r.takes(sg, i, s)) continue;
+                            const int sb = r.b % L::kNS;
+                            if (!(ok = wait(L::kPReady + sb, r.b / L::kNS))) break;
+                            tc_fence_after();
+                            const uint64_t v0 = vd + ((st * L::kTileBytes) >> 4);
+                            if (steps == kTile / 16) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
-                            umma_ss(tmem + sb * 128, q0 + off, k0 + off, id, kk > 0 ? 1u : 0u);
-                        }
-                        umma_commit(&bars[L::kSFull + sb]);
-                        ++r.b;
-                    }
-                    if (ok) umma_commit(&bars[L::kKEmpty + st]);
-                }
-                if (ok)
-                    for (int s = r.first; s <= r.last; ++s) umma_commit(&bars[L::kQFree + s]);
-                r.end_segment();
-            }
-        }
-        __syncwarp();
-    } else if (warp == 3) {
-        // ------------------------------------------------------ O += P V ------
-        if (elect_one()) {
-            const uint32_t id = idesc_bf16(128, D, false, true);
-            const uint64_t vd = desc_mnmajor_sw128(smem_u32(smem + L::kV), kSlab);
-            bool ok = true;
-            while (ok && next_seg_one()) {
-                r.segment(a, sg);
-                // the slots' accumulators must have been read out
-                for (int s = r.first; ok && s <= r.last; ++s)
-                    if (r.used(s) > 0) ok = wait(L::kOFree + s, r.used(s) - 1);
-                int begun = 0;                        // slots with a product in this segment (bits)
-                for (int i = sg.i0; ok && i < sg.i1; ++i, ++r.j) {
-                    const int st = r.j % L::kVS;
-                    const int steps = (tile_rows(a, sg, i) + 15) / 16;     // 16 keys each
-                    if (!(ok = wait(L::kVFull + st, r.j / L::kVS))) break;
-                    for (int s = r.first; s <= r.last; ++s) {
-                        if (!r.takes(sg, i, s)) continue;
-                        const int sb = r.b % L::kNS;
-                        if (!(ok = wait(L::kPReady + sb, r.b / L::kNS))) break;
-                        tc_fence_after();
-                        const uint64_t v0 = vd + ((st * L::kTileBytes) >> 4);
-                        if (steps == kTile / 16) {
-#pragma unroll
-                            for (int kk = 0; kk < kTile / 16; ++kk)
-                                umma_ts(tmem + L::kColO + s * D, tmem + sb * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
-                                        (begun >> s & 1) || kk > 0 ? 1u : 0u);
-                        } else {
+                                for (int kk = 0; kk < kTile / 16; ++kk)
+                                    umma_ts(tmem + L::kColO + s * D, tmem + sb * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
+                                            (begun >> s & 1) || kk > 0 ? 1u : 0u);
+                            } else {
 #pragma unroll 1
-                            for (int kk = 0; kk < steps; ++kk)
-                                umma_ts(tmem + L::kColO + s * D, tmem + sb * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
-                                        (begun >> s & 1) || kk > 0 ? 1u : 0u);
+                                for (int kk = 0; kk < steps; ++kk)
+                                    umma_ts(tmem + L::kColO + s * D, tmem + sb * 128 + kk * 8, v0 + kk * (2048 >> 4), id,
+                                            (begun >> s & 1) || kk > 0 ? 1u : 0u);
+                            }
+                            umma_commit(&bars[L::kSFree + sb]);
+                            begun |= 1 << s;
+                            ++r.b;
                         }
-                        umma_commit(&bars[L::kSFree + sb]);
-                        begun |= 1 << s;
-                        ++r.b;
+                        if (ok) umma_commit(&bars[L::kVEmpty + st]);
                     }
-                    if (ok) umma_commit(&bars[L::kVEmpty + st]);
+                    if (ok)
+                        for (int s = r.first; s <= r.last; ++s) umma_commit(&bars[L::kOFull + s]);
+                    r.end_segment();
                 }
-                if (ok)
-                    for (int s = r.first; s <= r.last; ++s) umma_commit(&bars[L::kOFull + s]);
-                r.end_segment();
             }
+            __syncwarp();
         }
-        __syncwarp();
-    }
     } else {
         // ------------------------------------------------------ softmax -------
         regs_inc<NQ == 1 ? 200 : 208>();
@@ -626,15 +628,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                         }
                         // p = 2^(s sl2 - m), packed
                         const float ref = m == -INFINITY ? 0.0f : m;     // a row that sees nothing yet: p = 0
-                        float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        // (multiply-adds and sums two at a time: 3% of the whole where blocks bound it)
+                        const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(-ref, -ref);
+                        uint64_t rs[2] = {0, 0};
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const float p0 = ex2(fmaf(__uint_as_float(x[2 * e]), sl2, -ref));
-                            const float p1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), sl2, -ref));
-                            rs[e & 3] += p0 + p1;
+                            float p0, p1;
+                            unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl22, ref2),
+                                    p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            rs[e & 1] = add2(rs[e & 1], pack2(p0, p1));
                             pk[e] = pack_bf16(p0, p1);
                         }
-                        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                        float l0, l1;
+                        unpack2(add2(rs[0], rs[1]), l0, l1);
+                        l += l0 + l1;
                     }
                 }
                 if (active) {
