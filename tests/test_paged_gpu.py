@@ -1,5 +1,7 @@
 """The paged calls on the GPU against the oracle: page plans, appends, tree
 masks, the attention of drafted tokens, and a run of them together."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -482,6 +484,167 @@ def test_tree_workspace_too_small():
         moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], y["mask"],
                               torch.empty_like(y["q"]), torch.empty(y["q"].shape[:2], device=DEV), ws, n - 1)
     assert err.value.status == moda.MODA_ERR_WORKSPACE
+
+
+# fp32 keeps blocks of 4, 16 or 64 rows, for requests of that many on average, and
+# tiles of 32 keys
+FP32 = [
+    Tree(held=(700, 33, 0), new=(1, 1, 1), Hq=8, Hk=2, L=0),
+    Tree(held=(9000,), new=(1,), Hq=4, Hk=1, L=31, page=64, chain=True),          # cut over many CTAs
+    Tree(held=(31, 32, 33), new=(1, 1, 1), L=48, chain=True),                     # more depth rows than a tile
+    Tree(held=(95, 96), new=(4, 4), Hq=2, Hk=2, L=33, d=64),                      # G = 1
+    Tree(held=(64, 200), new=(1, 1), Hq=6, Hk=2, L=32, d=64, window=7),           # G = 3
+    Tree(held=(500, 31), new=(4, 2), Hq=8, Hk=2, L=31),                           # 16 rows
+    Tree(held=(40, 160), new=(3, 3), Hq=10, Hk=2, L=32, d=64, chain=True),        # G = 5: 3 tokens in 15 rows
+    Tree(held=(77, 3), new=(1, 1), Hq=16, Hk=1, L=2),                             # G = 16
+    Tree(held=(1, 1, 1, 1), new=(16, 0, 0, 0), Hq=4, Hk=1, L=3, d=64),            # one request has all: 4 of 4 rows
+    Tree(held=(333,), new=(40,), Hq=8, Hk=2, L=5, page=8),                        # 64 rows
+    Tree(held=(2500, 70), new=(17, 50), Hq=12, Hk=2, L=40, d=64, page=16, pad=4), # G = 6
+]
+
+
+@pytest.mark.parametrize("c", FP32, ids=str)
+def test_tree_fp32_blocks(c):
+    c = dataclasses.replace(c, dtype="fp32")
+    x, see, sh = make_tree(c)
+    o, lse = run_tree(to_device(x), sh)
+    check_tree(c, x, see, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tree_outputs_at_any_16_bytes(dtype):
+    """Inputs, outputs and workspace that begin on odd multiples of 16 bytes."""
+    c = Tree(held=(300, 20), new=(9, 2), L=5, dtype=dtype)
+    x, see, sh = make_tree(c)
+    y = to_device(x)
+
+    def shifted(t):
+        n = 16 // t.element_size()
+        flat = torch.zeros(t.numel() + 2 * n, dtype=t.dtype, device=DEV)
+        at = flat[n:n + t.numel()] if flat.data_ptr() % 32 == 0 else flat[2 * n:2 * n + t.numel()]
+        assert at.data_ptr() % 32 == 16
+        return at.view(t.shape).copy_(t)
+    y = {k: (None if t is None else shifted(t)) for k, t in y.items()}
+    n = moda.moda_tree_decode_workspace_size(sh)
+    ws = shifted(torch.zeros(n, dtype=torch.uint8, device=DEV))
+    o, lse = shifted(torch.full_like(y["q"], float("nan"))), shifted(torch.full(y["q"].shape[:2], float("nan"), device=DEV))
+    moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], y["mask"], o, lse,
+                          ws, n)
+    check_tree(c, x, see, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_and_tree_past_32_bit_offsets(dtype):
+    """Pages whose elements begin behind 2^32."""
+    c = Tree(held=(1500, 40), new=(5, 3), Hq=4, Hk=2, L=2, page=1024, dtype=dtype)
+    x, see, sh = make_tree(c)
+    n_big = 2 ** 32 // (c.Hk * c.page * c.d) + sh.n_pages
+    y = to_device(x)
+    new_k, new_v, slots = [], [], []
+    used = [int(p) for b, (h, n) in enumerate(zip(c.held, c.new)) for p in x["table"][b, : -(-(h + n) // c.page)]]
+    for k, rows in (("kc", new_k), ("vc", new_v)):
+        big = torch.empty((n_big, *x[k].shape[1:]), dtype=x[k].dtype, device=DEV)
+        for p in used:
+            big[n_big - 1 - p] = y[k][p]
+        for b in range(2):
+            for t in range(c.held[b], c.held[b] + c.new[b]):
+                p = n_big - 1 - int(x["table"][b, t // c.page])
+                rows.append(big[p, :, t % c.page].clone())
+                big[p, :, t % c.page] = float("nan")
+                if k == "kc":
+                    slots.append(p * c.page + t % c.page)
+        y[k] = big
+    y["table"] = torch.where(y["table"] < sh.n_pages, n_big - 1 - y["table"], y["table"]).to(torch.int32)
+    sh.n_pages = n_big
+    moda.moda_cache_append(sh, torch.stack(new_k), torch.stack(new_v), torch.tensor(slots, device=DEV), y["kc"], y["vc"])
+    o, lse = run_tree(y, sh)
+    check_tree(c, x, see, o, lse)
+
+
+def test_plan_past_32_bit_slots():
+    P, n_pages = 1024, 3 << 20
+    fl, count = torch.arange(n_pages, dtype=torch.int32, device=DEV), dev_i32([n_pages])
+    table = table_of([[], []], 3)
+    cu, granted, slots = run_plan(P, 1030, [0, 0], [1025, 2], table, fl, count, n_pages)
+    assert cu == [0, 1025, 1027] and granted == [1025, 2] and int(count) == n_pages - 3
+    top = n_pages - 1
+    assert table.tolist() == [[top, top - 1, -1], [top - 2, -1, -1]]
+    assert slots == ([top * P + i for i in range(1024)] + [(top - 1) * P] + [(top - 2) * P, (top - 2) * P + 1] + [-1] * 3)
+
+
+def test_plan_most_requests():
+    B, P = 16384, 8
+    rng = np.random.default_rng(5)
+    held = rng.integers(0, 30, B)
+    want = np.where(rng.random(B) < 0.2, 0, held + rng.integers(0, 5, B))
+    rows, free = start_pages(rng, held, P, sum(-(-int(h) // P) for h in held) + 1000)
+    n_pages = sum(map(len, rows)) + len(free)
+    N = int(np.maximum(want - held, 0).sum()) + 1
+    table, fl, count = table_of(rows, 5), dev_i32(free + [-7] * (n_pages - len(free))), dev_i32([len(free)])
+    ref = oracle.page_plan(held, want, {"rows": rows, "max_pages": 5}, free, P, N)
+    cu, granted, slots = run_plan(P, N, held, want, table, fl, count, n_pages)
+    assert granted == ref[1] and cu == ref[0] and slots == ref[2]
+    assert torch.equal(table, table_of(ref[3], 5)) and fl.tolist()[: len(ref[4])] == ref[4]
+
+
+def test_tree_two_graphs_at_once():
+    """Two captured calls, a workspace each, replayed on two streams at the same time."""
+    cases = [Tree(held=(900, 70, 333), new=(9, 30, 2), L=4), Tree(held=(50,) * 40, new=(3,) * 40, L=2, seed=2)]
+    runs = []
+    for c in cases:
+        x, see, sh = make_tree(c)
+        y = to_device(x)
+        n = moda.moda_tree_decode_workspace_size(sh)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        o, lse = torch.full_like(y["q"], float("nan")), torch.full(y["q"].shape[:2], float("nan"), device=DEV)
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"],
+                                      y["mask"], o, lse, ws, n)
+        runs.append((c, x, see, graph, s, o, lse, y, ws))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for r in runs:
+            with torch.cuda.stream(r[4]):
+                r[3].replay()
+    torch.cuda.synchronize()
+    for c, x, see, _, _, o, lse, *_ in runs:
+        check_tree(c, x, see, o, lse)
+
+
+def test_step_captured_over_two_streams():
+    """Append on a side stream beside the mask, joined before the attention, as one graph."""
+    c = Tree(held=(200, 31), new=(12, 5), L=3)
+    rng = np.random.default_rng(3)
+    parent = random_parents(c.new, rng)
+    see, pos_ref = oracle.tree_mask(parent, np.concatenate([[0], np.cumsum(c.new)]), list(c.held))
+    x, see, sh = make_tree(c, see)
+    y = to_device(x)
+    slots = [int(x["table"][b, t // c.page]) * c.page + t % c.page
+             for b in range(2) for t in range(c.held[b], c.held[b] + c.new[b])]
+    at = torch.tensor(slots)
+    k, v = (x[n][at // c.page, :, at % c.page].contiguous().to(DEV) for n in ("kc", "vc"))
+    y["kc"][at // c.page, :, at % c.page] = float("nan")
+    y["vc"][at // c.page, :, at % c.page] = float("nan")
+    par, mask, pos = dev_i32(parent), torch.zeros_like(y["mask"]), torch.zeros(len(slots), dtype=torch.int32, device=DEV)
+    at = at.to(DEV)
+    n = moda.moda_tree_decode_workspace_size(sh)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    o, lse = torch.full_like(y["q"], float("nan")), torch.full(y["q"].shape[:2], float("nan"), device=DEV)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        moda.moda_cache_append(sh, k, v, at, y["kc"], y["vc"], stream=side)
+        moda.moda_tree_mask(sh, par, y["cu"], y["held"], mask, pos)
+        main.wait_stream(side)
+        moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], mask, o, lse,
+                              ws, n)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert pos.tolist() == pos_ref.tolist()
+    check_tree(c, x, see, o, lse)
 
 
 # ------------------------------------------------------------------- together --
