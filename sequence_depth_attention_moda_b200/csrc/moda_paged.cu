@@ -522,7 +522,8 @@ moda_status guarded(F&& f) noexcept {
 // length, every new token's depth rows in a tile of their own.
 static double most_cost(const Paged& p, const TreePlan& t) {
     const double groups = p.B + double(p.N) / t.Tg;
-    return p.Hk * (groups * (double(p.max_pages) * p.page / t.KT + 1) * t.tiles + double(p.N) * t.dsplit);
+    return p.Hk * (groups * ((double(p.max_pages) * p.page / t.KT + 1) * t.tiles + t.job_cost) +
+                   double(p.N) * t.dsplit);
 }
 
 TreePlan tree_plan(const Paged& p) {
@@ -553,6 +554,10 @@ TreePlan tree_plan(const Paged& p) {
         t.Lp = Lw;
         t.n_cta = 2 * device_sm_count();
     }
+    // A job's beginning in tiles.  Uneven requests, job_cost = 0, 1, 2, 3, 4: bf16, 48 of up
+    // to 64 tokens over 4096 keys 98, 92, 88, 87, 87 us; 32 of up to 200 161, 154, 143, 141,
+    // 138; fp32, 64 of one token over 1000 keys 70, 64, 57, 56, 58; even ones: no change.
+    t.job_cost = 3;
     t.Tg = t.Tq * t.tiles;
     t.dtok = Lw <= t.KT ? t.KT / t.Lp : 1;
     t.dsplit = (Lw + t.KT - 1) / t.KT;
@@ -710,6 +715,7 @@ moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const
         a.page_shift = p.page_shift; a.n_pages = p.n_pages; a.max_pages = p.max_pages; a.words = p.words;
         a.Tq = t.Tq; a.Tg = t.Tg; a.KT = t.KT; a.Lp = t.Lp; a.dtok = t.dtok; a.dsplit = t.dsplit;
         a.two_cost = t.tiles;
+        a.job_cost = t.job_cost;
         while ((1 << a.kt_shift) < t.KT) ++a.kt_shift;
         a.rec_rows = t.rec_rows; a.n_cta = t.n_cta; a.scale_log2 = p.scale_log2;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -10,9 +10,11 @@
 // Only the keys from `held` on and the depth rows are masked.  The jobs' tiles
 // form one list, in the order request, KV head, group, tile; each has a cost (a
 // sequence tile that two row tiles take costs more than one that a single one
-// takes), and CTA c of P owns the tiles that begin in the c-th of P equal parts
-// of the total cost X (X < 2^31, which the host checks, so 32 bits and no long
-// division; X / P is at least the largest cost, so that no part is empty).  Lengths live on the
+// takes, and a job's beginning costs job_cost: the pipeline drains and fills, Q is
+// fetched and O written), and CTA c of P owns the tiles that begin in the c-th of
+// P equal parts of the total cost X (X < 2^31, which the host checks, so 32 bits
+// and no long division; X / P is at least the largest tile's cost, so that a part
+// between two of a job's tiles has one of them itself).  Lengths live on the
 // device (a captured graph replays with other ones), so every CTA adds up the
 // list itself.  A job that one CTA owns whole is written out by it; of a job
 // cut at a range's end every CTA leaves one (m, l, o) record a row, and the
@@ -64,6 +66,7 @@ struct TreeArgs {
     int Lp, dtok, dsplit;                // depth tiles: rows a token takes, tokens per tile (Lw <= KT),
                                          // tiles per token (Lw > KT)
     int two_cost;                        // cost of a sequence tile that two row tiles take: 1 or 2 (others: 1)
+    int job_cost;                        // of a job's beginning, before its first tile
     int rec_rows, n_cta;
     float scale_log2;
 };
@@ -106,10 +109,11 @@ struct Job {
     int cseq, cost;      // cost of a sequence tile (1 or 2), of the job
 };
 // Where tile i of a job begins, and the first tile that begins at x or behind.
-__device__ __forceinline__ int tile_begin(const Job& j, int i) {
-    return i + min(i, j.nseq) * (j.cseq - 1);
+__device__ __forceinline__ int tile_begin(const TreeArgs& a, const Job& j, int i) {
+    return a.job_cost + i + min(i, j.nseq) * (j.cseq - 1);
 }
-__device__ __forceinline__ int tile_from(const Job& j, int x) {
+__device__ __forceinline__ int tile_from(const TreeArgs& a, const Job& j, int x) {
+    x -= a.job_cost;
     if (x <= 0) return 0;
     if (x <= j.nseq * j.cseq) return (x + j.cseq - 1) >> (j.cseq - 1);
     return min(j.nt, x - j.nseq * (j.cseq - 1));
@@ -129,7 +133,7 @@ __device__ __forceinline__ void set_group(const TreeArgs& a, Job& j, int group) 
     j.ndep0 = dep_tiles_of(a, min(j.ntok, a.Tq));
     j.nt = j.nseq + j.ndep0 + dep_tiles_of(a, j.ntok - a.Tq);
     j.cseq = j.ntok > a.Tq ? a.two_cost : 1;
-    j.cost = j.nt + j.nseq * (j.cseq - 1);
+    j.cost = a.job_cost + j.nt + j.nseq * (j.cseq - 1);
 }
 
 // Cost of one KV head of a request.
@@ -254,10 +258,10 @@ struct Walk {
         j = s.j;
         look_ahead(a);
         end = s.lo + s.length;
-        take(tile_from(j, s.lo));
-        // the part may begin behind the job's last tile's beginning: then it has
-        // none of this job (nor does the combine kernel look for it)
+        take(a, tile_from(a, j, s.lo));
         seg = 0;
+        // the part may begin behind the job's last tile's beginning, or end before the
+        // first one's: then it has none of this job (nor does the combine kernel look for it)
         return i0 < i1 || next_job(a);
     }
     __device__ __forceinline__ bool next(const TreeArgs& a) {
@@ -273,7 +277,7 @@ struct Walk {
    private:
     __device__ __forceinline__ bool next_job(const TreeArgs& a) {
         end -= j.cost;
-        if (end <= 0) return false;
+        if (end <= a.job_cost) return false;
         int g = j.group + 1;
         if (g * a.Tg >= j.r.n) {
             g = 0;
@@ -287,15 +291,15 @@ struct Walk {
             }
         }
         set_group(a, j, g);
-        take(0);
+        take(a, 0);
         return true;
     }
     __device__ __forceinline__ void look_ahead(const TreeArgs& a) {
         if (j.b + 1 < a.B) ahead = load_raw(a, j.b + 1);
     }
-    __device__ __forceinline__ void take(int first) {
+    __device__ __forceinline__ void take(const TreeArgs& a, int first) {
         i0 = first;
-        i1 = tile_from(j, end);
+        i1 = tile_from(a, j, end);
     }
 };
 
@@ -405,7 +409,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 struct TreePlan {
     int rows, KT;            // query rows per row tile, keys per tile
     int tiles;               // row tiles per job (1 or 2)
-    int Tq, Tg, Lp, dtok, dsplit, rec_rows, n_cta;
+    int Tq, Tg, Lp, dtok, dsplit, rec_rows, n_cta, job_cost;
     size_t off_ml, off_po, bytes;
 };
 TreePlan tree_plan(const Paged& p);

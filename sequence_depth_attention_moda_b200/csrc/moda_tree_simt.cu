@@ -401,8 +401,8 @@ cudaError_t launch_d(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
 }
 
 // Merges the records of a job that range ends cut: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
-// CTA (c, y) looks at the job that holds range c's first tile, and works if c
-// is the first range end inside that job; a warp takes one row.
+// CTA (c, y) looks at the job in which part c begins, and works if the part before
+// holds the job's first tile and some other its last one; a warp takes one row.
 constexpr int kCombineWarps = 8;
 constexpr int kBatch = 8;
 
@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     set_group(a, j, h.group);
     // The parts that hold the beginnings of the job's first and last tile.  Part c
     // is the one to work if it is the second of several.
-    const int first = range_of(h.job_start, h.x_total, P);
-    const int last = range_of(h.job_start + tile_begin(j, j.nt - 1), h.x_total, P);
+    const int first = range_of(h.job_start + tile_begin(a, j, 0), h.x_total, P);
+    const int last = range_of(h.job_start + tile_begin(a, j, j.nt - 1), h.x_total, P);
     if (c != first + 1 || last == first) return;
     const int n = last - first + 1;
     auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(first + i) + (i == 0); };   // see Walk::slot
