@@ -91,9 +91,8 @@ struct Lay {
     static constexpr uint32_t kSeg = kStart + (sizeof(Start) + 15) / 16 * 16;
     static constexpr uint32_t kMisc = kSeg + kSegs * sizeof(Seg);       // tmem base, abort flag, marks
     static constexpr uint32_t kBytes = kMisc + 16 + kMarks * 4;
-    static constexpr uint32_t kDynSmem = kBytes + 1024;     // alignment slack
     static_assert(kColO + NQ * D <= kTmemCols, "TMEM columns");
-    static_assert(kDynSmem <= 232448, "shared memory of one CTA");
+    static_assert(kBytes <= 232448, "shared memory of one CTA");
     static_assert(kKS + kNS + 2 < kSegs && kVS + 2 < kSegs, "segments in flight");
 };
 
@@ -280,9 +279,7 @@ template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_constant__ SmArgs g) {
     using L = Lay<D, NQ>;
     const TreeArgs& a = g.t;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char smem[];      // (TMA's and the descriptors' 128-byte swizzle)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
     Start* start = reinterpret_cast<Start*>(smem + L::kStart);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMisc);
@@ -789,7 +786,7 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
         g.tvd = g.tv;
     }
     const void* f = reinterpret_cast<const void*>(tree_sm100_kernel<D, NQ>);
-    if ((e = set_max_dynamic_smem(f, Lay<D, NQ>::kDynSmem)) != cudaSuccess) return e;
+    if ((e = set_max_dynamic_smem(f, Lay<D, NQ>::kBytes)) != cudaSuccess) return e;
     // set up (barriers, TMEM) while the grid before it in the stream ends
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -797,7 +794,7 @@ cudaError_t launch_d(const Paged& p, const TreePlan& t, const TreeArgs& a, cudaS
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(t.n_cta);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Lay<D, NQ>::kDynSmem;
+    cfg.dynamicSmemBytes = Lay<D, NQ>::kBytes;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
