@@ -22,8 +22,8 @@
 // share a block always adjacent, R = 64 took 680 us where it now takes 533).
 //
 // Measured (8 requests, 32 query heads over 8, d 128, 8192 keys each): 1 token
-// 146 us (R = 4; keys and values of 0.54 GB at 3.7 TB/s), 4 tokens 233 (R = 16),
-// 16 tokens 533 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
+// 143 us (R = 4; keys and values of 0.54 GB at 3.8 TB/s), 4 tokens 232 (R = 16),
+// 16 tokens 535 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
 // reads 8 vectors for 64 multiply-adds, and larger blocks do not fit the registers of
 // two CTAs an SM).  One tile in flight and plain loads: 359, 363 and 743 us.
 #include "moda_tree.cuh"
@@ -403,6 +403,8 @@ cudaError_t launch_d(const TreePlan& t, const TreeArgs& a, cudaStream_t s) {
 // Merges the records of a job that range ends cut: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
 // CTA (c, y) looks at the job in which part c begins, and works if the part before
 // holds the job's first tile and some other its last one; a warp takes one row.
+// Bound by latency (headers, records, outputs: three dependent accesses, about 3 us
+// behind the grid it waits for); up to kBatch records of a row are in flight.
 constexpr int kCombineWarps = 8;
 constexpr int kBatch = 8;
 

@@ -60,6 +60,7 @@ def start_pages(rng, held, P, n_pages):
 PLANS = [  # B, P, most held, most added, spare pages
     (1, 8, 0, 1, 1), (1, 64, 1, 0, 0), (7, 16, 100, 40, 100), (300, 8, 50, 20, 2000), (513, 32, 10, 3, 900),
     (4, 16, 5000, 9000, 4000), (64, 128, 3000, 700, 5), (40, 8, 100, 100, 0), (1000, 1024, 5000, 3, 700),
+    (4500, 8, 10, 1, 100),      # more requests than tokens
 ]
 
 
