@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* marks = reinterpret_cast<volatile int*>(tmem_holder + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);    // known to be uniform
 
     // the combine kernel may be set up now; it waits for this grid on the device
     griddep_launch_dependents();
