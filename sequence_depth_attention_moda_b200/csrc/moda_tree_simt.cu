@@ -22,8 +22,8 @@
 // share a block always adjacent, R = 64 took 680 us where it now takes 533).
 //
 // Measured (8 requests, 32 query heads over 8, d 128, 8192 keys each): 1 token
-// 143 us (R = 4; keys and values of 0.54 GB at 3.8 TB/s), 4 tokens 232 (R = 16),
-// 16 tokens 535 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
+// 142 us (R = 4; keys and values of 0.54 GB at 3.8 TB/s), 4 tokens 237 (R = 16),
+// 16 tokens 523 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
 // reads 8 vectors for 64 multiply-adds, and larger blocks do not fit the registers of
 // two CTAs an SM).  One tile in flight and plain loads: 359, 363 and 743 us.
 #include "moda_tree.cuh"
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
     const int cg = kStep == 1 ? tid / DS % 8 : tid % 8;       // keys cg + 8c of S, columns 4cg + 32j of O
     const int rg = tid / DS / 8;          // rows 4rg .. 4rg+3
     const int page = 1 << a.page_shift;
+    const int wr0 = 4 * ((tid & ~31) / DS / 8), wr1 = 4 * ((tid | 31) / DS / 8) + 4;      // the warp's rows
 
     for (bool first = true;; first = false) {
         __syncthreads();                  // the previous job is done with shared memory
@@ -233,35 +234,46 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
+            // Whether any of the warp's rows sees any of the tile's: not those behind the last
+            // token, nor, in a depth tile, other tokens' rows (their p will be 0).  22 requests of
+            // up to 78 tokens over 221 keys: 103 us without, 97 with.
+            bool mine = true;
+            if (R > 4 && wr0 >= rows) mine = false;
+            if (R > 4 && dep) {
+                const int tok = a.Lw <= a.KT ? dt * a.dtok : dt / a.dsplit, n = a.Lw <= a.KT ? a.dtok : 1;
+                mine = mine && wr0 < (tok + n) * a.G && wr1 > tok * a.G;
+            }
             // S: 4 rows x 4 keys over this lane's share of the head dimension
-            float s[16] = {};             // [row][key]
+            if (mine) {
+                float s[16] = {};             // [row][key]
 #pragma unroll 4
-            for (int d = ds * 4; d < D; d += 4 * DS) {
-                float4 qv[4];
+                for (int d = ds * 4; d < D; d += 4 * DS) {
+                    float4 qv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sq[(4 * rg + i) * L::kPitch + d]);
+                    for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sq[(4 * rg + i) * L::kPitch + d]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 kv = *reinterpret_cast<const float4*>(&sk[(cg + 8 * c) * L::kPitch + d]);
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 kv = *reinterpret_cast<const float4*>(&sk[(cg + 8 * c) * L::kPitch + d]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float x = s[4 * r + c];
-                        x = fmaf(qv[r].x, kv.x, x);
-                        x = fmaf(qv[r].y, kv.y, x);
-                        x = fmaf(qv[r].z, kv.z, x);
-                        s[4 * r + c] = fmaf(qv[r].w, kv.w, x);
+                        for (int r = 0; r < 4; ++r) {
+                            float x = s[4 * r + c];
+                            x = fmaf(qv[r].x, kv.x, x);
+                            x = fmaf(qv[r].y, kv.y, x);
+                            x = fmaf(qv[r].z, kv.z, x);
+                            s[4 * r + c] = fmaf(qv[r].w, kv.w, x);
+                        }
                     }
                 }
-            }
-            group_sum<16, DS, kStep>(s, ds);
-            {
-                constexpr int mine = DS <= 16 ? 16 / DS : 1;
-                const int first = DS <= 16 ? ds * mine : ds / (DS / 16);
-                if (DS <= 16 || ds % (DS / 16) == 0) {
+                group_sum<16, DS, kStep>(s, ds);
+                {
+                    constexpr int part = DS <= 16 ? 16 / DS : 1;
+                    const int first = DS <= 16 ? ds * part : ds / (DS / 16);
+                    if (DS <= 16 || ds % (DS / 16) == 0) {
 #pragma unroll
-                    for (int i = 0; i < mine; ++i) {
-                        const int x = first + i;             // row x / 4, key x % 4 of the block
-                        sp[(4 * rg + x / 4) * (kKeys + 4) + cg + 8 * (x % 4)] = s[i];
+                        for (int i = 0; i < part; ++i) {
+                            const int x = first + i;             // row x / 4, key x % 4 of the block
+                            sp[(4 * rg + x / 4) * (kKeys + 4) + cg + 8 * (x % 4)] = s[i];
+                        }
                     }
                 }
             }
@@ -300,29 +312,31 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
                 if (sub == 0) salpha[srw] = alpha;
             }
             __syncthreads();
-            // O = O alpha + P V over this lane's share of the keys
+            // O = O alpha + P V over this lane's share of the keys (alpha is 1 where p is 0)
+            if (mine) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float al = salpha[4 * rg + r];
+                for (int r = 0; r < 4; ++r) {
+                    const float al = salpha[4 * rg + r];
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
+                    for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[r][c][e] *= al;
-            }
+                        for (int e = 0; e < 4; ++e) o[r][c][e] *= al;
+                }
 #pragma unroll 2
-            for (int k = ds; k < kKeys; k += DS) {
-                float p[4];
+                for (int k = ds; k < kKeys; k += DS) {
+                    float p[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = sp[(4 * rg + r) * (kKeys + 4) + k];
+                    for (int r = 0; r < 4; ++r) p[r] = sp[(4 * rg + r) * (kKeys + 4) + k];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(&sv[k * L::kPitch + 4 * cg + 32 * c]);
+                    for (int c = 0; c < NC; ++c) {
+                        const float4 v = *reinterpret_cast<const float4*>(&sv[k * L::kPitch + 4 * cg + 32 * c]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        o[r][c][0] = fmaf(p[r], v.x, o[r][c][0]);
-                        o[r][c][1] = fmaf(p[r], v.y, o[r][c][1]);
-                        o[r][c][2] = fmaf(p[r], v.z, o[r][c][2]);
-                        o[r][c][3] = fmaf(p[r], v.w, o[r][c][3]);
+                        for (int r = 0; r < 4; ++r) {
+                            o[r][c][0] = fmaf(p[r], v.x, o[r][c][0]);
+                            o[r][c][1] = fmaf(p[r], v.y, o[r][c][1]);
+                            o[r][c][2] = fmaf(p[r], v.z, o[r][c][2]);
+                            o[r][c][3] = fmaf(p[r], v.w, o[r][c][3]);
+                        }
                     }
                 }
             }

@@ -36,7 +36,7 @@
 //
 // Measured (32 query heads over 8, d 128, 48 depth rows, 8 requests of 32768 keys):
 // 1 token 172 us, 6.2 TB/s, where the bytes alone take 164; 32 tokens 201 to 205, and
-// 231 once the power cap has brought the clock to 1.4 GHz: a tile's block then takes
+// 225 once the power cap has brought the clock to 1.4 GHz: a tile's block then takes
 // the softmax warps as long as HBM its bytes.  A block takes about 2000 cycles, of
 // which 1024 are exponentials (16 a cycle) and 1024 tensor work; the rest is latency
 // of two warps a sub-partition.  48 ragged requests of up to 64 tokens over 4096 keys
