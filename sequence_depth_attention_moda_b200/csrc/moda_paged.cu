@@ -545,13 +545,16 @@ TreePlan tree_plan(const Paged& p) {
         // Two row tiles a job read the keys once for 256 rows, but leave two score
         // buffers instead of three, and a job's blocks run one after the other on one
         // SM.  Where requests fill more than one tile and the cache (as far as the
-        // shape tells) is several times L2, the bytes win: n = 64, G = 4, d = 128, 8
-        // heads, 8 requests: T = 32768 321 us against 368, T = 12288 143 against 151,
-        // T = 8192 108 against 103, T = 4096 75 against 66.  With d = 64 a tile's bytes
-        // are half and its exponentials the same: T = 32768 272 against 257.
+        // shape tells) is more than L2 keeps, the bytes win, the sooner the more tiles
+        // read them again.  G = 4, d = 128, 8 heads, 8 requests, one tile against two:
+        // n = 64 over 4096 keys (cache of 137 MB) 65, 71 us; 8192 (270 MB) 98, 103; 9000
+        // (297 MB) 108, 106; 10500 127, 118; 32768 362, 301.  n = 128 over 4096 101, 113;
+        // 8192 196, 176.  n = 256 over 4096 (143 MB) 185, 191; 8192 347, 326.  n = 1000 over
+        // 4096 (167 MB) 818, 789.  With d = 64 a tile's bytes are half and its exponentials
+        // the same: n = 64 over 32768 257, 272.
         const double pages = double(p.B) * p.max_pages < p.n_pages ? double(p.B) * p.max_pages : p.n_pages;
         const double cache = pages * p.page * p.Hk * p.d * 2 * p.elem_bytes;
-        t.tiles = per > t.Tq && p.d == 128 && cache > 320e6 ? 2 : 1;
+        t.tiles = per > t.Tq && p.d == 128 && cache > (per > 2 * t.Tq ? 160e6 : 280e6) ? 2 : 1;
         t.Lp = (Lw + 7) / 8 * 8;       // a token's depth rows begin on a swizzle atom
         t.n_cta = device_sm_count();
     } else {
