@@ -338,8 +338,11 @@ typedef struct moda_paged_shape {
  * The list is a stack, and a call that gives back exactly what the last call
  * took restores it.  held_len is not changed; granted_len is the next call's
  * held_len, in a buffer of its own (it may alias neither length).  B <= 16384.  Deterministic.
- * Out of range: lengths are cut to 0..max_pages*page_size; new tokens behind N
- * get no slot; a free_count above n_pages counts as n_pages.
+ * Out of range: held_len is cut to 0..max_pages*page_size and a negative want_len
+ * counts as 0; new tokens behind N get no slot; a free_count above n_pages counts
+ * as n_pages.  A table entry that names no page is not given back: it is set to -1
+ * and the list does not grow by it.  A list entry that names none is taken off and
+ * entered in the table as -1.  New tokens on a page that is none get slot -1.
  */
 moda_status moda_page_plan(const moda_paged_shape* shape, const int* held_len, const int* want_len,
                            int* block_table, int* free_pages, int* free_count, int* cu_new,

@@ -261,10 +261,13 @@ def tree_decode(q, kc, vc, Kd, Vd, table, held, cu, see=None, window: int = 0, s
     return o, lse
 
 
-def page_plan(held, want, table, free, P: int, N: int):
+def page_plan(held, want, table, free, P: int, N: int, n_pages=None):
     """Pages and slots from lengths, request by request with a list as the
     stack (last entry on top).  table is a list of lists of pages (only the
-    pages held).  Returns (cu, granted, slots [N], table, free)."""
+    pages held).  Returns (cu, granted, slots [N], table, free).  With n_pages,
+    entries outside 0..n_pages-1 name no page: released ones are dropped, those
+    taken off the list are entered as -1, and their tokens have slot -1."""
+    is_page = lambda p: n_pages is None or 0 <= p < n_pages  # noqa: E731
     max_pages = table["max_pages"]
     rows = [list(r) for r in table["rows"]]
     free = list(free)
@@ -274,7 +277,7 @@ def page_plan(held, want, table, free, P: int, N: int):
         if n_of(want[b]) <= max_pages:
             released += rows[b][n_of(want[b]):n_of(held[b])]
             del rows[b][n_of(want[b]):]
-    free += released[::-1]                      # the first request's first page on top
+    free += [p for p in released[::-1] if is_page(p)]     # the first request's first page on top
     granted, asked, top = [], 0, len(free)
     for b in range(len(held)):
         take = n_of(want[b]) - n_of(held[b]) if n_of(want[b]) <= max_pages else 0
@@ -283,12 +286,13 @@ def page_plan(held, want, table, free, P: int, N: int):
         if n_of(want[b]) > max_pages or (take > 0 and asked > top):
             granted.append(int(held[b]))
             continue
-        rows[b] += [free.pop() for _ in range(take)]
+        rows[b] += [p if is_page(p) else -1 for p in (free.pop() for _ in range(take))]
         granted.append(int(want[b]))
     cu, slots = [0], []
     for b in range(len(held)):
         for key in range(int(held[b]), granted[b]):
-            slots.append(rows[b][key // P] * P + key % P)
+            page = rows[b][key // P]
+            slots.append(page * P + key % P if is_page(page) else -1)
         cu.append(len(slots))
     slots = (slots + [-1] * N)[:N]
     return cu, granted, slots, rows, free

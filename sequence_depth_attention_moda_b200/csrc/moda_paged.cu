@@ -27,6 +27,8 @@ namespace {
 // a call took restores the list.  A request is served whole or not at all: if it
 // needs no page, or take_b + its own pages <= top; those that are served pages
 // come before those that are refused some, so pages 0 .. granted-1 are theirs.
+// Released entries that name no page (a held length beyond the pages a request has)
+// are counted first and do not count in top: they never get on the list.
 //
 // Bound by latency, not by bytes.  Every CTA adds up all requests (8 KB for 1024
 // of them) and keeps the prefixes in shared memory; then a thread finds its
@@ -111,6 +113,10 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanArgs& a, int b) {
     return r;
 }
 
+__device__ __forceinline__ bool is_page(const PlanArgs& a, int page) {
+    return static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
+}
+
 // The last of n entries of an ascending list that is <= x (the first is 0).
 __device__ __forceinline__ int last_at_most(const int* list, int n, int x) {
     int lo = 0, hi = n - 1;
@@ -137,7 +143,8 @@ __device__ __forceinline__ void write_slots(const PlanArgs& a, const int* s_cu, 
             const int held = static_cast<int>(min(static_cast<long long>(max(__ldg(a.held + b), 0)), cap));
             const int key = held + static_cast<int>(t - s_cu[b]);
             const int page = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
-            if (page >= 0) slot[u] = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            if (is_page(a, page)) slot[u] = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            else atomicOr(a.status, kStatusBadIndex);
         }
     }
 #pragma unroll
@@ -147,10 +154,28 @@ __device__ __forceinline__ void write_slots(const PlanArgs& a, const int* s_cu, 
     }
 }
 
+// The sum over the grid of each CTA's *x, which is in shared memory, behind a barrier.
+template <int CTAS>
+__device__ __forceinline__ int grid_sum(const int* x) {
+    plan_barrier<CTAS>();
+    if (CTAS == 1) return *x;
+    int sum = 0;
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) {
+        uint32_t at;
+        int y;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(x)), "r"(r));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
+        sum += y;
+    }
+    return sum;
+}
+
 template <int CTAS>
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int plan_smem[];
     __shared__ longlong2 warp_sum[kPlanWarps];
+    __shared__ int s_lost;
     int* s_cu = plan_smem;               // [B+1] prefixes of tokens,
     int* s_take = s_cu + a.B + 1;        // [B]   of pages asked for,
     int* s_drop = s_take + a.B;          // [B]   of pages given back
@@ -170,20 +195,45 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         drop += max(r.have - r.need, 0);
     }
     block_prefix(take, drop, warp_sum, &takes, &drops);
-    const int count = min(max(count0, 0), a.n_pages);
-    const long long top = count + drops;
-    if (count != count0 || top > a.n_pages) atomicOr(a.status, kStatusBadIndex);
-    // what is served: its tokens and pages
-    long long tokens = 0, pages = 0, n_tokens, granted;
     {
         long long at = take, dr = drop;
         for (int b = b0; b < b1; ++b) {
             const PlanRequest r = plan_request(a, b);
-            const int t = max(r.need - r.have, 0);
             s_take[b] = static_cast<int>(at);
             s_drop[b] = static_cast<int>(dr);
-            at += t;
+            at += max(r.need - r.have, 0);
             dr += max(r.have - r.need, 0);
+        }
+    }
+    // released entries that name no page
+    auto released = [&](long long x) -> int* {
+        const int b = last_at_most(s_drop, a.B, static_cast<int>(x));
+        return a.table + static_cast<size_t>(b) * a.max_pages + plan_request(a, b).need + (x - s_drop[b]);
+    };
+    int lost = 0, page0 = -1;            // page0: this thread's first
+    if (drops > 0) {
+        if (tid == 0) s_lost = 0;
+        __syncthreads();
+        int mine = 0;
+        for (long long x = all; x < drops; x += CTAS * kPlanThreads) {
+            const int page = __ldcg(released(x));
+            if (x == all) page0 = page;
+            mine += !is_page(a, page);
+        }
+        if (mine > 0) atomicAdd(&s_lost, mine);
+        lost = grid_sum<CTAS>(&s_lost);
+    }
+    const int count = min(max(count0, 0), a.n_pages);
+    const long long top = count + drops - lost;
+    if (count != count0 || lost > 0 || top > a.n_pages) atomicOr(a.status, kStatusBadIndex);
+    // what is served: its tokens and pages
+    long long tokens = 0, pages = 0, n_tokens, granted;
+    {
+        long long at = take;
+        for (int b = b0; b < b1; ++b) {
+            const PlanRequest r = plan_request(a, b);
+            const int t = max(r.need - r.have, 0);
+            at += t;
             if (r.fits && (t == 0 || at <= top)) {
                 tokens += max(r.want - r.held, 0);
                 pages += t;
@@ -214,22 +264,39 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     __syncthreads();
 
     // released pages onto the list
-    for (int x = all; x < static_cast<int>(drops); x += CTAS * kPlanThreads) {
-        const int b = last_at_most(s_drop, a.B, x);
-        int* entry = a.table + static_cast<size_t>(b) * a.max_pages + plan_request(a, b).need + (x - s_drop[b]);
-        const int page = __ldcg(entry);
-        const long long place = top - 1 - x;
-        if (place < a.n_pages) a.free_pages[place] = page;
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) atomicOr(a.status, kStatusBadIndex);
-        *entry = -1;
+    if (lost == 0) {
+        for (long long x = all; x < drops; x += CTAS * kPlanThreads) {
+            int* entry = released(x);
+            const int page = x == all ? page0 : __ldcg(entry);
+            const long long place = top - 1 - x;
+            if (place < a.n_pages) a.free_pages[place] = page;
+            *entry = -1;
+        }
+    } else if (rank == 0) {              // (rare) counted past those that name none, by one CTA
+        long long before = 0;
+        for (long long x0 = 0; x0 < drops; x0 += kPlanThreads) {
+            const long long x = x0 + tid;
+            int* entry = x < drops ? released(x) : nullptr;
+            const int page = entry ? __ldcg(entry) : -1;
+            long long at = is_page(a, page), none = 0, n, n_none;
+            block_prefix(at, none, warp_sum, &n, &n_none);
+            const long long place = top - 1 - before - at;
+            if (is_page(a, page) && place < a.n_pages) a.free_pages[place] = page;
+            if (entry) *entry = -1;
+            before += n;
+        }
     }
     plan_barrier<CTAS>();
     // asked-for pages off it
-    for (int x = all; x < static_cast<int>(granted); x += CTAS * kPlanThreads) {
-        const int b = last_at_most(s_take, a.B, x);
+    for (long long x = all; x < granted; x += CTAS * kPlanThreads) {
+        const int b = last_at_most(s_take, a.B, static_cast<int>(x));
         const long long place = top - 1 - x;
-        a.table[static_cast<size_t>(b) * a.max_pages + plan_request(a, b).have + (x - s_take[b])] =
-            place < a.n_pages ? __ldcg(a.free_pages + place) : -1;
+        int page = place < a.n_pages ? __ldcg(a.free_pages + place) : -1;
+        if (!is_page(a, page)) {
+            page = -1;
+            atomicOr(a.status, kStatusBadIndex);
+        }
+        a.table[static_cast<size_t>(b) * a.max_pages + plan_request(a, b).have + (x - s_take[b])] = page;
     }
     if (rank == 0 && tid == 0) *a.free_count = static_cast<int>(min(top - granted, static_cast<long long>(a.n_pages)));
     if (!a.slots_here) return;

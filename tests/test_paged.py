@@ -107,6 +107,19 @@ def test_plan_oracle_gives_back_what_it_took():
     assert rows3 == rows and free3 == free and back == held.tolist() and set(slots3) == {-1}
 
 
+def test_plan_oracle_drops_what_names_no_page():
+    P = 8
+    table = {"rows": [[5, 2, -1, 99], [], [7]], "max_pages": 6}
+    cu, granted, slots, rows, free = oracle.page_plan([32, 0, 3], [0, 17, 5], table, [3, 1], P, 20, n_pages=10)
+    # pages 5 and 2 come back, the other two entries do not; three pages are asked for
+    assert granted == [0, 17, 5] and cu == [0, 0, 17, 19] and free == [3]
+    assert rows == [[], [5, 2, 1], [7]]
+    assert slots == [5 * P + i for i in range(8)] + [2 * P + i for i in range(8)] + [P] + [7 * P + 3, 7 * P + 4, -1]
+    # an entry of the list that names none is entered as -1, and its tokens have no slot
+    cu, granted, slots, rows, free = oracle.page_plan([0], [9], {"rows": [[]], "max_pages": 6}, [4, -3, 6], P, 9, n_pages=10)
+    assert granted == [9] and rows == [[6, -1]] and slots == [6 * P + i for i in range(8)] + [-1] and free == [4]
+
+
 # ------------------------------------------------------------------- refusals --
 def base(**kw):
     b = dict(B=2, N=8, Hq=8, Hk=2, d=128, L=4, page_size=16, n_pages=10, max_pages=4, mask_words=1)

@@ -132,6 +132,57 @@ def test_plan_out_of_range_lengths():
     assert granted == [8] and slots == list(range(8, 16)) and count.tolist() == [1]
 
 
+def test_plan_bad_pages_do_not_reach_the_list():
+    """A held length beyond the pages a request has: the entries that name no
+    page are reported and not given back, so the next call gets pages only."""
+    P, mp = 8, 6
+    table = table_of([[5, 2, -1, 1 << 30], [7]], mp)
+    fl, count = dev_i32([3, 1, -9, -9, -9, -9, -9, -9]), dev_i32([2])
+    cu, granted, slots = run_plan(P, 0, [32, 3], [0, 3], table, fl, count, 8)
+    bad_status()
+    assert granted == [0, 3] and count.tolist() == [4] and fl.tolist()[:4] == [3, 1, 2, 5]
+    assert table.tolist() == [[-1] * mp, [7] + [-1] * 5]
+    cu, granted, slots = run_plan(P, 40, [0, 3], [32, 8], table, fl, count, 8)
+    moda.moda_check_status()
+    assert granted == [32, 8] and table.tolist() == [[5, 2, 1, 3, -1, -1], [7] + [-1] * 5] and count.tolist() == [0]
+    assert slots == [p * P + i for p in (5, 2, 1, 3) for i in range(P)] + [7 * P + i for i in range(3, 8)] + [-1] * 3
+
+
+def test_plan_list_entry_that_names_no_page():
+    P, mp = 8, 4
+    for bad in (-1, 6, 1 << 30):
+        table, fl, count = table_of([[], []], mp), dev_i32([0, bad, 4, -1, -1, -1]), dev_i32([3])
+        cu, granted, slots = run_plan(P, 30, [0, 0], [9, 2], table, fl, count, 6)
+        bad_status()
+        assert granted == [9, 2] and count.tolist() == [0] and table.tolist() == [[4, -1, -1, -1], [0, -1, -1, -1]]
+        assert slots == [4 * P + i for i in range(8)] + [-1, 0, 1] + [-1] * 19
+    # tokens added to a last page that is none
+    table, fl, count = table_of([[3, -1]], mp), dev_i32([0, 1, 2, -1, -1, -1]), dev_i32([3])
+    cu, granted, slots = run_plan(P, 12, [10], [18], table, fl, count, 6)
+    bad_status()
+    assert granted == [18] and table.tolist() == [[3, -1, 2, -1]]
+    assert slots == [-1] * 6 + [16, 17] + [-1] * 4
+
+
+@pytest.mark.parametrize("B,N", [(40, 3000), (900, 40), (900, 400000), (4500, 60000)])
+def test_plan_random_bad_pages(B, N):
+    """One CTA and the cluster, slots in the plan and apart."""
+    P, mp = 8, 12
+    rng = np.random.default_rng(B + N)
+    held = rng.integers(0, P * mp + 1, B)
+    want = np.where(rng.random(B) < 0.5, 0, rng.integers(0, P * mp + 9, B))
+    n_pages = sum(-(-int(h) // P) for h in held) + 50
+    rows, free = start_pages(rng, held, P, n_pages)
+    rows = [[p if rng.random() > 0.1 else int(rng.choice([-1, n_pages, -2 ** 31, 2 ** 31 - 1])) for p in r] for r in rows]
+    table, fl, count = table_of(rows, mp), dev_i32(free + [-7] * (n_pages - len(free))), dev_i32([len(free)])
+    ref = oracle.page_plan(held, want, {"rows": rows, "max_pages": mp}, free, P, N, n_pages=n_pages)
+    cu, granted, slots = run_plan(P, N, held, want, table, fl, count, n_pages)
+    bad_status()
+    assert granted == ref[1] and cu == ref[0] and slots == ref[2]
+    assert torch.equal(table, table_of(ref[3], mp))
+    assert count.tolist() == [len(ref[4])] and fl.tolist()[: len(ref[4])] == ref[4]
+
+
 # --------------------------------------------------------------------- append --
 @pytest.mark.parametrize("N,Hk,d,P,dtype", [(1, 1, 64, 8, "bf16"), (5, 3, 64, 16, "fp32"), (257, 2, 128, 64, "bf16"),
                                             (1000, 8, 128, 8, "fp32"), (4099, 5, 64, 1024, "bf16")])
