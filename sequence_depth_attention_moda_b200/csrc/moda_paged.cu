@@ -28,7 +28,7 @@ namespace {
 // needs no page, or take_b + its own pages <= top; those that are served pages
 // come before those that are refused some, so pages 0 .. granted-1 are theirs.
 // Released entries that name no page (a held length beyond the pages a request has)
-// are counted first and do not count in top: they never get on the list.
+// are counted while they are moved and taken out again: they do not count in top.
 //
 // Bound by latency, not by bytes.  Every CTA adds up all requests (8 KB for 1024
 // of them) and keeps the prefixes in shared memory; then a thread finds its
@@ -171,6 +171,29 @@ __device__ __forceinline__ int grid_sum(const int* x) {
     return sum;
 }
 
+// The table's entry for released page x of the call; s_drop: prefixes of those pages.
+__device__ __forceinline__ int* released_entry(const PlanArgs& a, const int* s_drop, unsigned x) {
+    const int b = last_at_most(s_drop, a.B, static_cast<int>(x));
+    return a.table + static_cast<size_t>(b) * a.max_pages + plan_request(a, b).need + (static_cast<int>(x) - s_drop[b]);
+}
+
+// (Rare; one CTA.)  Of `drops` released entries the pages alone go to places count, count + 1, ..
+// of the list: taken from its places count .., or, if they are not there, from the table.
+__device__ __noinline__ void pack_released(const PlanArgs& a, const int* s_drop, longlong2* warp_sum, int count,
+                                           long long drops, bool listed) {
+    long long place = count;
+    for (long long i0 = 0; i0 < drops; i0 += kPlanThreads) {
+        const long long i = i0 + threadIdx.x;
+        int* entry = i >= drops ? nullptr : (listed ? a.free_pages + count + i : released_entry(a, s_drop, static_cast<unsigned>(drops - 1 - i)));
+        const int page = entry ? __ldcg(entry) : -1;
+        long long at = is_page(a, page), none = 0, n, n_none;
+        block_prefix(at, none, warp_sum, &n, &n_none);       // (all have read before any writes)
+        if (is_page(a, page) && place + at < a.n_pages) a.free_pages[place + at] = page;
+        if (entry && !listed) *entry = -1;
+        place += n;
+    }
+}
+
 template <int CTAS>
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int plan_smem[];
@@ -184,46 +207,47 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     const int all = rank * kPlanThreads + tid;                          // thread of the grid
     const int ch = (a.B + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
+    if (tid == 0) s_lost = 0;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
     const int count0 = __ldcg(a.free_count);
+    PlanRequest r0 = {};                 // up to 1024 requests have a thread each
+    if (b0 < b1) r0 = plan_request(a, b0);
     long long take = 0, drop = 0, takes, drops;
     for (int b = b0; b < b1; ++b) {
-        const PlanRequest r = plan_request(a, b);
+        const PlanRequest r = b == b0 ? r0 : plan_request(a, b);
         take += max(r.need - r.have, 0);
         drop += max(r.have - r.need, 0);
     }
     block_prefix(take, drop, warp_sum, &takes, &drops);
-    {
-        long long at = take, dr = drop;
-        for (int b = b0; b < b1; ++b) {
-            const PlanRequest r = plan_request(a, b);
-            s_take[b] = static_cast<int>(at);
-            s_drop[b] = static_cast<int>(dr);
-            at += max(r.need - r.have, 0);
-            dr += max(r.have - r.need, 0);
-        }
-    }
-    // released entries that name no page
-    auto released = [&](long long x) -> int* {
-        const int b = last_at_most(s_drop, a.B, static_cast<int>(x));
-        return a.table + static_cast<size_t>(b) * a.max_pages + plan_request(a, b).need + (x - s_drop[b]);
-    };
-    int lost = 0, page0 = -1;            // page0: this thread's first
+    // released pages onto the list
+    const int count = min(max(count0, 0), a.n_pages);
+    const bool room = count + drops <= a.n_pages;      // else some of them cannot be pages, or the list is wrong
+    int lost = 0;                        // entries that name no page
     if (drops > 0) {
-        if (tid == 0) s_lost = 0;
+        for (int b = b0; b < b1; ++b) {
+            const PlanRequest r = b == b0 ? r0 : plan_request(a, b);
+            s_drop[b] = static_cast<int>(drop);
+            drop += max(r.have - r.need, 0);
+        }
         __syncthreads();
         int mine = 0;
-        for (long long x = all; x < drops; x += CTAS * kPlanThreads) {
-            const int page = __ldcg(released(x));
-            if (x == all) page0 = page;
+        for (unsigned x = all; x < static_cast<unsigned>(drops); x += CTAS * kPlanThreads) {
+            int* entry = released_entry(a, s_drop, x);
+            const int page = __ldcg(entry);
             mine += !is_page(a, page);
+            if (!room) continue;
+            a.free_pages[count + static_cast<int>(drops) - 1 - static_cast<int>(x)] = page;
+            *entry = -1;
         }
         if (mine > 0) atomicAdd(&s_lost, mine);
         lost = grid_sum<CTAS>(&s_lost);
+        if (lost > 0 || !room) {         // (rare) one CTA moves the pages together, from the list's bottom
+            if (rank == 0) pack_released(a, s_drop, warp_sum, count, drops, room);
+            plan_barrier<CTAS>();
+        }
     }
-    const int count = min(max(count0, 0), a.n_pages);
     const long long top = count + drops - lost;
     if (count != count0 || lost > 0 || top > a.n_pages) atomicOr(a.status, kStatusBadIndex);
     // what is served: its tokens and pages
@@ -231,8 +255,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     {
         long long at = take;
         for (int b = b0; b < b1; ++b) {
-            const PlanRequest r = plan_request(a, b);
+            const PlanRequest r = b == b0 ? r0 : plan_request(a, b);
             const int t = max(r.need - r.have, 0);
+            s_take[b] = static_cast<int>(at);
             at += t;
             if (r.fits && (t == 0 || at <= top)) {
                 tokens += max(r.want - r.held, 0);
@@ -243,7 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     block_prefix(tokens, pages, warp_sum, &n_tokens, &granted);
     long long c = tokens, at = take;
     for (int b = b0; b < b1; ++b) {
-        const PlanRequest r = plan_request(a, b);
+        const PlanRequest r = b == b0 ? r0 : plan_request(a, b);
         const int t = max(r.need - r.have, 0);
         at += t;
         const bool served = r.fits && (t == 0 || at <= top);
@@ -263,32 +288,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     }
     __syncthreads();
 
-    // released pages onto the list
-    if (lost == 0) {
-        for (long long x = all; x < drops; x += CTAS * kPlanThreads) {
-            int* entry = released(x);
-            const int page = x == all ? page0 : __ldcg(entry);
-            const long long place = top - 1 - x;
-            if (place < a.n_pages) a.free_pages[place] = page;
-            *entry = -1;
-        }
-    } else if (rank == 0) {              // (rare) counted past those that name none, by one CTA
-        long long before = 0;
-        for (long long x0 = 0; x0 < drops; x0 += kPlanThreads) {
-            const long long x = x0 + tid;
-            int* entry = x < drops ? released(x) : nullptr;
-            const int page = entry ? __ldcg(entry) : -1;
-            long long at = is_page(a, page), none = 0, n, n_none;
-            block_prefix(at, none, warp_sum, &n, &n_none);
-            const long long place = top - 1 - before - at;
-            if (is_page(a, page) && place < a.n_pages) a.free_pages[place] = page;
-            if (entry) *entry = -1;
-            before += n;
-        }
-    }
-    plan_barrier<CTAS>();
     // asked-for pages off it
-    for (long long x = all; x < granted; x += CTAS * kPlanThreads) {
+    for (unsigned x = all; x < static_cast<unsigned>(granted); x += CTAS * kPlanThreads) {
         const int b = last_at_most(s_take, a.B, static_cast<int>(x));
         const long long place = top - 1 - x;
         int page = place < a.n_pages ? __ldcg(a.free_pages + place) : -1;
@@ -296,11 +297,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
             page = -1;
             atomicOr(a.status, kStatusBadIndex);
         }
-        a.table[static_cast<size_t>(b) * a.max_pages + plan_request(a, b).have + (x - s_take[b])] = page;
+        a.table[static_cast<size_t>(b) * a.max_pages + plan_request(a, b).have + (static_cast<int>(x) - s_take[b])] = page;
     }
     if (rank == 0 && tid == 0) *a.free_count = static_cast<int>(min(top - granted, static_cast<long long>(a.n_pages)));
+    if (a.slots_here || (CTAS > 1 && drops > 0)) plan_barrier<CTAS>();   // (or: until grid_sum's reads are done)
     if (!a.slots_here) return;
-    plan_barrier<CTAS>();
     for (long long t0 = (all >> 5) * 32ll * kSlotsPerLane; t0 < a.N; t0 += CTAS * kPlanThreads * kSlotsPerLane)
         write_slots(a, s_cu, t0, lane);
 }
