@@ -370,6 +370,7 @@ moda_status moda_cache_append(const moda_paged_shape* shape, const void* k_new, 
  *                  tokens
  * A request may have at most 32*mask_words new tokens.  Out of range: tokens
  * behind those get no row, and a parent that is no earlier token counts as -1.
+ * Where cu_new descends, a row that several requests claim holds one's.
  */
 moda_status moda_tree_mask(const moda_paged_shape* shape, const int* parent, const int* cu_new,
                            const int* held_len, unsigned int* mask, int* position,
@@ -398,7 +399,7 @@ moda_status moda_tree_mask(const moda_paged_shape* shape, const int* parent, con
  * weights rounded to bf16 for the product with V.
  * Out of range: lengths are cut to the table, to N and to 32*mask_words new
  * tokens (rows behind those are not written), and a table entry that names no
- * page reads as zeros.
+ * page reads as zeros.  If cu_new descends anywhere, no row is written.
  */
 size_t moda_tree_decode_workspace_size(const moda_paged_shape* shape);
 moda_status moda_tree_decode(const moda_paged_shape* shape, const void* q, const void* k_cache,

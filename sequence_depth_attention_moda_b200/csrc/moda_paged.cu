@@ -446,9 +446,8 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const __grid_co
     const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
     const int h = a.held ? __ldg(a.held + b) : 0;
     const int first = min(max(c0, 0), a.N);
-    const int n = static_cast<int>(max(0ll, min(static_cast<long long>(c1) - c0,
-                                                min(static_cast<long long>(a.N - first), 32ll * a.words))));
-    bool bad = first != c0 || n != c1 - c0;
+    const int n = max(0, min(min(max(c1, 0), a.N) - first, 32 * a.words));
+    bool bad = first != c0 || n != static_cast<long long>(c1) - c0;
     if (i0 >= n && i0 > 0) return;
     for (int i = threadIdx.x; i < min(n, i0 + kMaskThreads); i += kMaskThreads) {
         int p = __ldg(a.parent + first + i);

@@ -16,7 +16,8 @@
 // and no long division; X / P is at least the largest tile's cost, so that a part
 // between two of a job's tiles has one of them itself).  Lengths live on the
 // device (a captured graph replays with other ones), so every CTA adds up the
-// list itself.  A job that one CTA owns whole is written out by it; of a job
+// list itself.  Where cu_new descends the requests share rows and the host's bound
+// does not hold: then the list is empty.  A job that one CTA owns whole is written out by it; of a job
 // cut at a range's end every CTA leaves one (m, l, o) record a row, and the
 // combine kernel merges them in CTA order.  At most two of a CTA's jobs can be
 // cut (its first and its last), so the records take 2 slots a CTA whatever
@@ -85,12 +86,12 @@ __device__ __forceinline__ Request clamp_request(const TreeArgs& a, const RawReq
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
     r.held = static_cast<int>(min(static_cast<long long>(max(x.held, 0)), cap));
     r.cu0 = min(max(x.c0, 0), a.N);
-    long long n = static_cast<long long>(x.c1) - x.c0;
-    n = min(n, static_cast<long long>(a.N - r.cu0));
+    long long n = min(max(x.c1, 0), a.N) - r.cu0;
     n = min(n, cap - r.held);
     if (a.mask) n = min(n, 32ll * a.words);
     r.n = static_cast<int>(max(n, 0ll));
-    if (r.held != x.held || r.cu0 != x.c0 || r.n != x.c1 - x.c0) atomicOr(a.status, kStatusBadIndex);
+    if (r.held != x.held || r.cu0 != x.c0 || r.n != static_cast<long long>(x.c1) - x.c0)
+        atomicOr(a.status, kStatusBadIndex);
     return r;
 }
 __device__ __forceinline__ Request load_request(const TreeArgs& a, int b) { return clamp_request(a, load_raw(a, b)); }
@@ -157,7 +158,7 @@ __device__ __forceinline__ int head_cost(const TreeArgs& a, const Request& r) {
 // Where a CTA starts, in shared memory; written by schedule().
 struct Start {
     int warp_sum[32];
-    int max_cost[32];
+    int max_cost[32];        // of a warp's sequence tiles, or kNoSchedule
     Job j;                   // the job in which the CTA's part begins,
     int lo;                  // and where in it
     int length;              // of the part; 0: none
@@ -174,6 +175,8 @@ __device__ __forceinline__ int range_of(int t, int x, int P) {
     return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q;
 }
 
+constexpr int kNoSchedule = 0x7fffffff;
+
 // Called by all threads of the CTA: finds the CTA's part and writes its header.
 // Ends with a __syncthreads.
 __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
@@ -183,8 +186,11 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
     Request r = {};
     int hc = 0, mine = 0, most = 1;
+    bool down = false;                   // cu_new descends
     for (int b = b0; b < b1; ++b) {
-        r = load_request(a, b);
+        const RawRequest raw = load_raw(a, b);
+        down |= raw.c1 < raw.c0;
+        r = clamp_request(a, raw);
         hc = head_cost(a, r);
         mine += hc * a.Hk;
         if (r.n > a.Tq) most = a.two_cost;
@@ -196,6 +202,7 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
         if (lane >= o) inc += up;
     }
     most = 1 + __any_sync(0xffffffffu, most > 1);
+    if (__any_sync(0xffffffffu, down)) most = kNoSchedule;
     if (lane == 31) {
         s->warp_sum[warp] = inc;
         s->max_cost[warp] = most;
@@ -209,7 +216,7 @@ __device__ __forceinline__ void schedule(const TreeArgs& a, Start* s) {
         total += s->warp_sum[w];
         most = max(most, s->max_cost[w]);
     }
-    const int P = min(a.n_cta, total / most), c = static_cast<int>(blockIdx.x);
+    const int P = most == kNoSchedule ? 0 : min(a.n_cta, total / most), c = static_cast<int>(blockIdx.x);
     if (c < P) {
         const int lo = range_begin(c, total, P);
         if (at <= lo && lo < at + mine) {

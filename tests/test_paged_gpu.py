@@ -460,6 +460,38 @@ def test_tree_out_of_range_lengths():
     assert bool(torch.isnan(o[32]).all()) and not bool(torch.isnan(o[:32]).any())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("chain", [True, False])
+def test_tree_starts_that_descend(dtype, chain):
+    """Requests that claim the same rows: reported, and no row is written."""
+    c = Tree(held=(10, 5, 7), new=(3, 2, 4), L=2, chain=chain, dtype=dtype)
+    x, see, sh = make_tree(c)
+    for cu in ([0, 9, 0, 9], [0, 3, 2, 9], [9, 5, 3, 0], [0, 3, 2 ** 31 - 1, -2 ** 31]):
+        x["cu"] = torch.tensor(cu, dtype=torch.int32)
+        o, lse = run_tree(to_device(x), sh)
+        bad_status()
+        assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tree_starts_outside_the_rows(dtype):
+    """Starts before the first row or behind the last: each request keeps its own rows."""
+    c = Tree(held=(10, 5, 7), new=(3, 2, 4), L=2, chain=True, dtype=dtype)
+    x, see, sh = make_tree(c)
+    for cu in ([-4, 3, 5, 9], [0, 3, 5, 40], [-2 ** 31, 3, 5, 2 ** 31 - 1]):
+        y = dict(x)
+        y["cu"] = torch.tensor(cu, dtype=torch.int32)
+        o, lse = run_tree(to_device(y), sh)
+        bad_status()
+        check_tree(c, x, see, o, lse)
+
+
+def test_mask_starts_out_of_range():
+    mask, pos = run_mask([-1, 0, -1, 0], [-3, 2, 9], [10, 20], 1, 4)
+    bad_status()
+    assert mask[:, 0].tolist() == [1, 3, 1, 3] and pos.tolist() == [10, 11, 20, 21]
+
+
 def test_tree_equals_decode():
     """One new token a request over equal lengths: moda_decode's result."""
     B, Hq, Hk, d, L, T, P = 3, 16, 4, 128, 5, 200, 16
