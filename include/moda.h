@@ -308,7 +308,8 @@ typedef struct moda_paged_shape {
     int L;            /* depth rows of a new token, >= 0                       */
     int page_size;    /* tokens a page: a power of two in 8..1024              */
     int n_pages;      /* pages of the cache, >= 1                              */
-    int max_pages;    /* columns of the block table, >= 1                      */
+    int max_pages;    /* columns of the block table, >= 1; B * max_pages < 2^31,
+                         max_pages * page_size <= 2^31 - 1024                  */
     int mask_words;   /* 32-bit words of a mask row, 0..64; 0: no mask (chain) */
     moda_dtype dtype; /* of q, caches, depth rows and o                        */
     float softmax_scale;  /* >= 0 and finite; 0 selects 1/sqrt(d)              */

@@ -496,8 +496,9 @@ moda_status check_pages(const moda_paged_shape* s, Paged* p) {
         return failf(MODA_ERR_INVALID_ARG, "page_size=%lld must be a power of two in 8..1024", s->page_size);
     if (s->n_pages < 1 || s->max_pages < 1)
         return failf(MODA_ERR_INVALID_ARG, "n_pages=%lld and max_pages=%lld must be >= 1", s->n_pages, s->max_pages);
-    // positions and table entries are indexed with 32 bits
-    if (static_cast<double>(s->max_pages) * s->page_size > 2147483647.0 ||
+    // positions and table entries are indexed with 32 bits, and so are the rows behind the last
+    // position of the tiles that are asked for ahead (fewer than 256)
+    if (static_cast<double>(s->max_pages) * s->page_size > 2147483648.0 - 1024.0 ||
         static_cast<double>(s->B) * s->max_pages > 2147483647.0)
         return failf(MODA_ERR_UNSUPPORTED, "max_pages=%lld too large for B=%lld requests of pages of %lld tokens",
                      s->max_pages, s->B, s->page_size);

@@ -170,6 +170,19 @@ def test_mask_rejects_bad_shapes(lib, kw, status):
     assert call(lib, "moda_tree_mask", base(**kw), 5) == status, moda.moda_last_error_message()
 
 
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 512, 1024])
+def test_table_length_leaves_room_for_a_tile(lib, page):
+    """Positions up to a tile behind the longest request fit 32 bits."""
+    most = (2 ** 31 - 1024) // page
+    for pages, ok in ((most, True), (most + 1, False), (2 ** 31 // page - 1, page == 1024)):
+        sh = base(B=1, Hq=2, Hk=1, page_size=page, max_pages=pages)
+        assert (lib.moda_tree_decode_workspace_size(ctypes.byref(sh)) != ctypes.c_size_t(-1).value) == ok
+        if ok:
+            continue
+        assert call(lib, "moda_tree_decode", sh, 12, 1 << 40) == moda.MODA_ERR_UNSUPPORTED
+        assert lib.moda_page_plan(ctypes.byref(sh), *[FAKE + 256 * i for i in range(8)], None) == moda.MODA_ERR_UNSUPPORTED
+
+
 def test_null_shape_and_pointers(lib):
     for name, n in (("moda_page_plan", 8), ("moda_cache_append", 5), ("moda_tree_mask", 5)):
         assert call(lib, name, None, n) == 1
