@@ -103,7 +103,7 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanArgs& a, int b) {
     PlanRequest r;
     const int P1 = (1 << a.page_shift) - 1;
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
-    const int h = __ldg(a.held + b), w = __ldg(a.want + b);
+    const int h = a.held[b], w = a.want[b];
     r.held = static_cast<int>(min(static_cast<long long>(max(h, 0)), cap));
     r.want = max(w, 0);
     if (r.held != h || r.want != w) atomicOr(a.status, kStatusBadIndex);
@@ -140,7 +140,7 @@ __device__ __forceinline__ void write_slots(const PlanArgs& a, const int* s_cu, 
         if (t < n_in) {
             while (s_cu[b + 1] <= t) ++b;
             const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
-            const int held = static_cast<int>(min(static_cast<long long>(max(__ldg(a.held + b), 0)), cap));
+            const int held = static_cast<int>(min(static_cast<long long>(max(a.held[b], 0)), cap));
             const int key = held + static_cast<int>(t - s_cu[b]);
             const int page = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
             if (is_page(a, page)) slot[u] = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
         const long long src = tok * a.row_chunks + c;
         dst[u] = -1;
         if (src >= a.n_chunks) continue;
-        const long long slot = __ldg(a.slots + tok);
+        const long long slot = a.slots[tok];
         if (slot >= 0 && slot < a.n_slots) {
             const unsigned hk = c / static_cast<unsigned>(a.head_chunks);
             const long long page = slot >> a.page_shift;
@@ -443,14 +443,14 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const __grid_co
     const int i0 = blockIdx.y * kMaskThreads;        // the CTA's first token
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-    const int h = a.held ? __ldg(a.held + b) : 0;
+    const int c0 = a.cu[b], c1 = a.cu[b + 1];
+    const int h = a.held ? a.held[b] : 0;
     const int first = min(max(c0, 0), a.N);
     const int n = max(0, min(min(max(c1, 0), a.N) - first, 32 * a.words));
     bool bad = first != c0 || n != static_cast<long long>(c1) - c0;
     if (i0 >= n && i0 > 0) return;
     for (int i = threadIdx.x; i < min(n, i0 + kMaskThreads); i += kMaskThreads) {
-        int p = __ldg(a.parent + first + i);
+        int p = a.parent[first + i];
         if (p < -1 || p >= i) {          // no earlier token: taken as the root's child
             bad = true;
             p = -1;

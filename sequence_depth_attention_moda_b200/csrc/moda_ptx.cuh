@@ -159,7 +159,8 @@ __device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint3
 // Programmatic dependent launch.  launch_dependents: this CTA lets a kernel
 // launched after it with programmatic stream serialization start; wait: until
 // the grid this kernel depends on has completed and its memory operations are
-// visible.
+// visible.  To ordinary loads: a read-only load (ld.global.nc) is for memory that
+// nobody writes while the kernel runs, and the grid it waits for does.
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -79,7 +79,7 @@ struct RawRequest {
     int held, c0, c1;
 };
 __device__ __forceinline__ RawRequest load_raw(const TreeArgs& a, int b) {
-    return RawRequest{__ldg(a.held + b), __ldg(a.cu + b), __ldg(a.cu + b + 1)};
+    return RawRequest{a.held[b], a.cu[b], a.cu[b + 1]};
 }
 __device__ __forceinline__ Request clamp_request(const TreeArgs& a, const RawRequest& x) {
     Request r;
@@ -324,7 +324,7 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
 __device__ __forceinline__ uint32_t mask_visible(const uint32_t* row, int words, int n, int rel) {
     if (rel <= -32) return 0xffffffffu;
     const int w = rel >> 5;             // floor
-    auto word = [&](int x) -> uint32_t { return x < 0 ? 0xffffffffu : (x < words ? __ldg(row + x) : 0u); };
+    auto word = [&](int x) -> uint32_t { return x < 0 ? 0xffffffffu : (x < words ? row[x] : 0u); };
     return __funnelshift_r(word(w), word(w + 1), rel & 31) & bits_between(0, n - rel);
 }
 // The same without a mask (a chain): the new keys up to the token itself.
@@ -351,7 +351,7 @@ __device__ __forceinline__ uint32_t dep_visible(const TreeArgs& a, int t, int dt
 // The block table's entry for a request's key `key`; the page an entry names, -1
 // (and a status) if it names none of the cache.
 __device__ __forceinline__ int table_entry(const TreeArgs& a, int b, int key) {
-    return __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
+    return a.table[static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift)];
 }
 __device__ __forceinline__ int checked_page(const TreeArgs& a, int p) {
     if (static_cast<unsigned>(p) < static_cast<unsigned>(a.n_pages)) return p;

@@ -1,6 +1,8 @@
 """The paged calls on the CPU: the oracle's own pins, and what the library and
 the binding refuse before anything reaches a device."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -253,6 +255,17 @@ def test_binding_rejects_bad_tensors(lib):
         moda.moda_cache_append(sh, bf(7, 2, 128), bf(8, 2, 128), torch.zeros(8, dtype=torch.int64), good["kc"], good["vc"])
     with pytest.raises(moda.MoDAError, match="parent holds"):
         moda.moda_tree_mask(sh, i32(7), i32(3), i32(2), i32(8, 1), i32(8))
+
+
+def test_dependent_launches_read_what_the_grid_before_wrote():
+    """A kernel that starts while the grid before it runs must not read that
+    grid's results (a plan's table, a mask) by read-only loads."""
+    names = [f for f in sorted(os.listdir(moda_build.CSRC)) if f.endswith((".cu", ".cuh"))]
+    text = {f: re.sub(r"//[^\n]*", "", open(os.path.join(moda_build.CSRC, f)).read()) for f in names}
+    waits = [f for f in names if "griddep_wait()" in text[f] and f != "moda_ptx.cuh"]
+    assert {"moda_paged.cu", "moda_tree_simt.cu", "moda_tree_sm100.cu"} <= set(waits)
+    for f in waits + ["moda_tree.cuh", "moda_ptx.cuh"]:
+        assert not re.search(r"__ldg|ld\.global\.nc", text[f]), f
 
 
 def test_random_parents_come_before():
