@@ -371,34 +371,108 @@ __device__ __forceinline__ int page_of(const TreeArgs& a, int b, int key) {
 // (rare) marked rows add them here, to the outputs just stored and each from
 // the keys it sees.  Added without its weight: p > 0 does not change an
 // infinity or a NaN.
+//
+// A warp goes once over the keys and depth rows that any of its rows sees, whole rows
+// of V at a time, and notes for each column which of its rows see a +Inf and which a
+// -Inf (a NaN counts as both): the time is that of reading V.  A chain of
+// 4096 tokens with an infinity or NaN in three of 8 heads' values (32 query heads, d = 128):
+// 2.2 ms against 0.30 without, in fp32 6.5 against 4.4.  A walk over the keys for every
+// column of every row took 560 and 950 ms.
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Columns c0, c0 + step, ... (n of them) of output row `out`, stored before by the same thread.
-template <typename E, int D>
-__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Request r, int b, int hk, int token, E* out,
-                                            int c0, int step, int n) {
-    const int page = 1 << a.page_shift;
-    const size_t row = (static_cast<size_t>(r.cu0 + token) * a.Hk + hk) * a.L;
-    for (int x = 0; x < n; ++x) {
-        const int col = c0 + x * step;
-        float sum = to_float(out[col]);
-        auto add = [&](const E* p) {
-            const float v = to_float(*p);
-            if (!isfinite(v)) sum += v;
-        };
-        for (int k = 0; k < r.n; ++k) {
-            const int key = r.held + k;
-            if (!(seq_visible(a, r, token, key) & 1u)) continue;
-            const int p = page_of(a, b, key);
-            if (p < 0) continue;
-            add(static_cast<const E*>(a.vc) +
-                ((static_cast<size_t>(p) * a.Hk + hk) * page + (key & (page - 1))) * D + col);
+// Rows row0, row0 + step, ... (n <= 16 of them; row = token * G + head, from the
+// request's token tok0 on) of a KV head's outputs, which the warp's lanes stored before
+// (or others, and a barrier).  Whole warp.  kAhead: rows of V in flight, which bound the time and the
+// registers (a callee's count is its kernel's too).
+template <typename E, int D, int kAhead>
+__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Request r, int b, int hk, int tok0, int row0, int step, int n) {
+    constexpr int C = D / 32;            // columns C * lane .. of a row are the lane's
+    constexpr int kWords = C * static_cast<int>(sizeof(E)) / 4;
+    constexpr uint32_t kAll = 0xffffffffu;
+    union alignas(4 * kWords) Piece {
+        uint32_t w[kWords];
+        E e[C];
+        __device__ Piece() {}
+    };
+    const int lane = threadIdx.x & 31, page = 1 << a.page_shift;
+    const int token = tok0 + (row0 + min(lane, n - 1) * step) / a.G;     // of the lane's output row
+    const int last = tok0 + (row0 + (n - 1) * step) / a.G;
+    uint32_t seen[C] = {};               // bit i: output row i sees a +Inf, bit 16 + i: a -Inf
+    const int keys = a.mask ? r.n : last + 1;
+    int k = 0, t = tok0 + row0 / a.G, l = a.win_lo;      // next key; then next depth row
+#pragma unroll 1
+    while (k < keys || (l < a.L && t <= last)) {
+        // 32 rows of V: lane i's `off` says where row i begins (-1: nowhere), bit i of
+        // `vis` whether the lane's output row sees it
+        const bool dep = k >= keys;
+        const E* base = static_cast<const E*>(dep ? a.vd : a.vc);
+        long long off = -1;
+        uint32_t vis = 0;
+        if (!dep) {
+            if (lane < n) vis = seq_visible(a, r, token, r.held + k);
+            if (k + lane < keys) {
+                const int key = r.held + k + lane, p = page_of(a, b, key);
+                if (p >= 0) off = ((static_cast<long long>(p) * a.Hk + hk) * page + (key & (page - 1))) * D;
+            }
+            k += 32;
+        } else {
+            if (lane < n && token == t) vis = kAll;
+            if (l + lane < a.L) off = ((static_cast<long long>(r.cu0 + t) * a.Hk + hk) * a.L + l + lane) * D;
+            l += 32;
+            if (l >= a.L) {
+                l = a.win_lo;
+                ++t;
+            }
         }
-        for (int l = a.win_lo; l < a.L; ++l) add(static_cast<const E*>(a.vd) + (row + l) * D + col);
-        from_float(out + col, sum);
+        const uint32_t any = __reduce_or_sync(kAll, vis) & __ballot_sync(kAll, off >= 0);
+#pragma unroll 1
+        for (int k0 = 0; k0 < 32; k0 += kAhead) {
+            if ((any >> k0 & (kAll >> (32 - kAhead))) == 0u) continue;
+            Piece v[kAhead];
+            uint32_t acc = 0;            // zeros (of any sign) while all is finite
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const long long at = __shfl_sync(kAll, off, k0 + u);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) v[u].w[w] = 0u;
+                if (any >> (k0 + u) & 1u) v[u] = *reinterpret_cast<const Piece*>(base + at + C * lane);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w)
+                    acc = sizeof(E) == 2 ? ptx::not_finite_acc(v[u].w[w], acc)
+                                         : __float_as_uint(fmaf(__uint_as_float(v[u].w[w]), 0.0f, __uint_as_float(acc)));
+            if (!__any_sync(kAll, acc & (sizeof(E) == 2 ? 0x7fff7fffu : 0x7fffffffu))) continue;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const uint32_t rows = __ballot_sync(kAll, vis >> (k0 + u) & 1u);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const float x = to_float(v[u].e[c]);
+                    if (!(x < INFINITY)) seen[c] |= rows;
+                    if (!(x > -INFINITY)) seen[c] |= rows << 16;
+                }
+            }
+        }
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const int row = row0 + i * step;
+        E* out = static_cast<E*>(a.o) +
+                 (static_cast<size_t>(r.cu0 + tok0 + row / a.G) * a.Hq + hk * a.G + row % a.G) * D + C * lane;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint32_t is = seen[c] >> i & 0x10001u;
+            if (is == 0u) continue;
+            float x = to_float(out[c]);
+            if (is & 1u) x += INFINITY;
+            if (is >> 16) x -= INFINITY;
+            from_float(out + c, x);
+        }
     }
 }
 

@@ -81,6 +81,15 @@ __device__ __forceinline__ void group_sum(float* v, int ds) {
     }
 }
 
+// The infinities and NaN of a marked job's values (add_not_finite).  A call between the
+// jobs, where next to nothing is in registers: elsewhere it cost the tile loop some.
+template <int D, int R>
+__device__ __noinline__ void finish_job(const TreeArgs& a, const Job& j) {
+    constexpr int n = R < 8 ? 1 : R / 8;
+    const int rows = j.ntok * a.G, row0 = static_cast<int>(threadIdx.x >> 5) * n;
+    if (row0 < rows) add_not_finite<float, D, 4>(a, j.r, j.b, j.hk, j.tok0, row0, 1, min(n, rows - row0));
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_constant__ TreeArgs a) {
     using L = Lay<D, R>;
@@ -102,11 +111,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
     Walk& w = *reinterpret_cast<Walk*>(smem + L::kWalk);
     int* spoison = reinterpret_cast<int*>(&w + 1);
     int* smore = spoison + 1;
+    int* sfinish = smore + 1;             // the last job's outputs lack its infinities and NaN
 
+    const int tid = threadIdx.x;
+    if (tid == 0) *sfinish = 0;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     schedule(a, st);
-    const int tid = threadIdx.x;
     // A quarter warp reads eight 16-byte pieces at a time, free of bank conflicts if
     // it is eight parts of a block or eight blocks' same part.
     constexpr int kStep = DS < 8 ? 8 : 1;
@@ -117,8 +128,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
     const int wr0 = 4 * ((tid & ~31) / DS / 8), wr1 = 4 * ((tid | 31) / DS / 8) + 4;      // the warp's rows
 
     for (bool first = true;; first = false) {
-        __syncthreads();                  // the previous job is done with shared memory
+        __syncthreads();                  // the previous job is done with shared memory, its outputs are stored
+        if (*sfinish) {
+            finish_job<D, R>(a, w.j);
+            __syncthreads();
+        }
         if (tid == 0) {
+            *sfinish = 0;
             *smore = first ? w.begin(a, *st) : w.next(a);
             *spoison = 0;
         }
@@ -322,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[r][c][e] *= al;
                 }
-#pragma unroll 2
+#pragma unroll 8
                 for (int k = ds; k < kKeys; k += DS) {
                     float p[4];
 #pragma unroll
@@ -375,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
                     const int col = 4 * cg + 32 * c;
                     *reinterpret_cast<float4*>(out + col) =
                         make_float4(o[r][c][0] * inv, o[r][c][1] * inv, o[r][c][2] * inv, o[r][c][3] * inv);
-                    if (poison) add_not_finite<float, D>(a, j.r, j.b, j.hk, tk, out, col, 1, 4);
                 }
+                if (poison) *sfinish = 1;
                 if (cg == 0) a.lse[orow] = row_lse(mr, lr);
             } else {
                 const size_t rec = slot * a.rec_rows + row;
@@ -444,10 +460,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     if (c != first + 1 || last == first) return;
     const int n = last - first + 1;
     auto slot_of = [&](int i) -> size_t { return 2 * static_cast<size_t>(first + i) + (i == 0); };   // see Walk::slot
+    bool poison = false;
     for (int row = blockIdx.y * kCombineWarps + warp; row < j.ntok * a.G; row += gridDim.y * kCombineWarps) {
         // online over the records, kBatch of them in flight at a time
         float M = -INFINITY, l = 0.0f, acc[C] = {};
-        bool poison = false;
         for (int i0 = 0; i0 < n; i0 += kBatch) {
             float2 ml[kBatch];
             float v[kBatch][C];
@@ -485,8 +501,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
         for (int e = 0; e < C; ++e) from_float(static_cast<E*>(a.o) + orow * D + lane + 32 * e, acc[e] * inv);
-        if (poison) add_not_finite<E, D>(a, j.r, j.b, j.hk, tk, static_cast<E*>(a.o) + orow * D, lane, 32, C);
         if (lane == 0) a.lse[orow] = row_lse(ref, l);
+    }
+    if (poison) {                        // a record's mark is that of all its rows
+        __syncwarp();
+        const int step = gridDim.y * kCombineWarps, row0 = blockIdx.y * kCombineWarps + warp;
+        const int n = (j.ntok * a.G - row0 + step - 1) / step;           // (> 0: some row was marked)
+        for (int i = 0; i < n; i += 16)
+            add_not_finite<E, D, 4>(a, j.r, j.b, j.hk, j.tok0, row0 + i * step, step, min(16, n - i));
     }
 }
 

@@ -730,11 +730,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[L::kOFree + s]);
-                if (!real) continue;
-                if (whole) {
+                if (real && whole) {
                     const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + orow * D;
-                    __nv_bfloat16* dst = out + half * (D / 2);
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + orow * D + half * (D / 2);
 #pragma unroll
                     for (int c = 0; c < D / 2; c += 16) {
                         uint32_t v[8];
@@ -748,9 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                             *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
                         }
                     }
-                    if (poison) add_not_finite<__nv_bfloat16, D>(a, sg.r, sg.b, sg.hk, token, out, half * (D / 2), 1, D / 2);
                     if (half == 0) a.lse[orow] = row_lse(m, lt);
-                } else {
+                } else if (real) {
                     if (some) {
                         float* dst = a.po + rec * D + half * (D / 2);
 #pragma unroll
@@ -758,6 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_sm100_kernel(const __grid_co
                     }
                     // a slot without a block here (only depth tiles of the other one): an empty record
                     if (half == 0) a.ml[rec] = make_float2(m, poison ? -lt : lt);
+                }
+                if (poison && whole && row0 < n_tok * a.G) {
+                    __syncwarp();
+                    add_not_finite<__nv_bfloat16, D, 8>(a, sg.r, sg.b, sg.hk, sg.tok0 + r.sub(s) * a.Tq, row0, 1,
+                                                         min(16, n_tok * a.G - row0));
                 }
             }
             r.end_segment();

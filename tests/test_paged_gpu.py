@@ -404,6 +404,75 @@ def test_tree_not_finite_two_row_tiles():
     check_rows_not_finite(c, x, see, o, lse)
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "bf16"), (128, "fp32"), (64, "fp32")])
+def test_tree_not_finite_in_a_long_chain(d, dtype):
+    """Infinities and a NaN among a prompt's values: in the rows that see them and
+    nowhere else, every other bit as without them, and in the time of a few clean
+    calls (not of a walk over all keys for every column)."""
+    n, Hq, Hk, P = 4096, 32, 8, 64
+    g = torch.Generator().manual_seed(d)
+    dt = torch_dtype(dtype)
+    sh = moda.make_paged_shape(1, n, Hq, Hk, d, 0, P, n // P + 1, n // P + 1, 0, moda.MODA_FP32 if dtype == "fp32" else 0)
+    q, kc, vc = (torch.randn(*s, generator=g).to(dt).to(DEV) for s in ((n, Hq, d), *[(n // P + 1, Hk, P, d)] * 2))
+    x = dict(q=q, kc=kc, vc=vc, Kd=None, Vd=None, table=torch.arange(n // P + 1, dtype=torch.int32, device=DEV)[None].contiguous(),
+             held=dev_i32([17]), cu=dev_i32([0, n]), mask=None)
+    bad = ((900, 2, 5, float("inf")), (2501, 2, 5, float("-inf")), (30, 0, d - 1, float("nan")), (4000, 7, 0, float("inf")))
+    y = dict(x, vc=vc.clone())
+    for t, hk, col, v in bad:
+        x["vc"][(17 + t) // P, hk, (17 + t) % P, col] = 0
+        y["vc"][(17 + t) // P, hk, (17 + t) % P, col] = v
+    nws = moda.moda_tree_decode_workspace_size(sh)
+    ws = torch.empty(nws, dtype=torch.uint8, device=DEV)
+    outs, best = [], []
+    for z in (x, y):
+        o, lse = torch.empty_like(q), torch.empty(n, Hq, device=DEV)
+        times = []
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            moda.moda_tree_decode(sh, z["q"], z["kc"], z["vc"], None, None, z["table"], z["held"], z["cu"], None, o, lse, ws, nws)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        outs.append((o, lse))
+        best.append(min(times))
+    (o, lse), (o2, lse2) = outs
+    ref = o.clone()
+    for t, hk, col, v in bad:
+        ref[t:, hk * 4:hk * 4 + 4, col] += v
+    assert torch.equal(lse, lse2)
+    assert torch.equal(o2.isnan(), ref.isnan()) and int(ref.isnan().sum()) > 0 and int(ref.isinf().sum()) > 0
+    assert torch.equal(o2.nan_to_num(nan=0.0), ref.nan_to_num(nan=0.0))
+    print("clean %.3f ms, with infinities %.3f ms" % tuple(best))
+    assert best[1] < 10 * best[0], best
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("c", [
+    Tree(held=tuple(range(0, 400, 2)), new=tuple(1 + k % 3 for k in range(200)), Hq=4, Hk=2, L=2),      # whole jobs
+    Tree(held=(33,), new=(70,), L=40, window=33, page=8, d=64),
+    Tree(held=(2, 900), new=(45, 20), Hq=2, Hk=2, L=1, chain=True, d=64),
+    Tree(held=(70,), new=(5,), Hq=64, Hk=1, L=130, window=129),
+], ids=["whole_jobs", "window", "chain", "G64"])
+def test_tree_not_finite_anywhere(c, dtype):
+    """Infinities and NaN strewn over the new keys' values and the depth rows, those
+    outside the window among them."""
+    c = dataclasses.replace(c, dtype=dtype)
+    x, see, sh = make_tree(c)
+    rng = np.random.default_rng(7)
+    n = int(x["cu"][-1])
+    for i in range(30):
+        v = (float("inf"), float("-inf"), float("nan"))[i % 3]
+        b = int(rng.integers(len(c.held)))
+        key = c.held[b] + int(rng.integers(c.new[b]))
+        x["vc"][int(x["table"][b][key // c.page]), rng.integers(c.Hk), key % c.page, rng.integers(c.d)] = v
+        if c.L:
+            x["Vd"][rng.integers(n), rng.integers(c.Hk), rng.integers(c.L), rng.integers(c.d)] = v
+    o, lse = run_tree(to_device(x), sh)
+    assert not bool(torch.isfinite(o[:n].float()).all())
+    check_rows_not_finite(c, x, see, o, lse)
+
+
 def check_rows_not_finite(c, x, see, o, lse):
     from paged_cases import oracle_tree
     ref, rlse = oracle_tree(c, x, see)
