@@ -354,6 +354,20 @@ def test_tree_two_row_tiles(c):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,Hk,chain", [(385, 1, False), (800, 2, True), (1000, 1, False), (2100, 1, True)])
+def test_tree_more_requests_than_threads(B, Hk, chain, dtype):
+    """Several requests a thread in the schedule (384 or 256 threads add them up),
+    some without new tokens, some long enough to be cut."""
+    rng = np.random.default_rng(B)
+    held = tuple(int(h) for h in np.where(rng.random(B) < 0.02, rng.integers(500, 2000, B), rng.integers(0, 40, B)))
+    new = tuple(int(n) for n in np.where(rng.random(B) < 0.01, 20, rng.integers(0, 3, B)))
+    c = Tree(held=held, new=new, Hq=2 * Hk, Hk=Hk, d=64, L=1, page=16, chain=chain, dtype=dtype, pad=2)
+    x, see, sh = make_tree(c)
+    o, lse = run_tree(to_device(x), sh)
+    check_tree(c, x, see, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("held,L,n", [(0, 0, 40), (5, 0, 40), (0, 3, 9), (200, 2, 70)])
 def test_tree_any_mask(dtype, held, L, n):
     """Masks that are no trees: rows without themselves, rows that see nothing
