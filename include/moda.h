@@ -301,7 +301,7 @@ moda_status moda_decode(const moda_shape* shape, const void* q, const void* K, c
  * moda_check_status as MODA_ERR_INVALID_ARG.
  */
 typedef struct moda_paged_shape {
-    int B;            /* requests, >= 0                                        */
+    int B;            /* requests, 0 .. 2^31 - 1024                            */
     int N;            /* rows of the token arrays, >= 0                        */
     int Hq, Hk;       /* heads, as in moda_shape; G = Hq / Hk <= 64            */
     int d;            /* 64 or 128                                             */

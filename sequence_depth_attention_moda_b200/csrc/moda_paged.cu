@@ -494,6 +494,8 @@ moda_status check_pages(const moda_paged_shape* s, Paged* p) {
     if (s->B < 0 || s->N < 0) return failf(MODA_ERR_INVALID_ARG, "B=%lld N=%lld must be >= 0", s->B, s->N);
     if (!power_of_two(s->page_size) || s->page_size < 8 || s->page_size > 1024)
         return failf(MODA_ERR_INVALID_ARG, "page_size=%lld must be a power of two in 8..1024", s->page_size);
+    // (a thread's share of the requests is rounded up in 32 bits)
+    if (s->B > 2147483647 - 1024) return failf(MODA_ERR_UNSUPPORTED, "B=%lld requests are too many", s->B);
     if (s->n_pages < 1 || s->max_pages < 1)
         return failf(MODA_ERR_INVALID_ARG, "n_pages=%lld and max_pages=%lld must be >= 1", s->n_pages, s->max_pages);
     // positions and table entries are indexed with 32 bits, and so are the rows behind the last
@@ -604,7 +606,8 @@ static double most_cost(const Paged& p, const TreePlan& t) {
 
 TreePlan tree_plan(const Paged& p) {
     TreePlan t;
-    const int per = p.B > 0 ? (p.N + p.B - 1) / p.B : p.N;     // tokens of a request, on average
+    // tokens of a request, on average
+    const int per = p.B > 0 ? static_cast<int>((static_cast<long long>(p.N) + p.B - 1) / p.B) : p.N;
     const int Lw = p.Lw > 0 ? p.Lw : 1;
     t.tiles = 1;
     if (p.elem_bytes == 2) {           // tensor cores: 128-row tiles, one CTA an SM

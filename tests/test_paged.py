@@ -172,6 +172,16 @@ def test_mask_rejects_bad_shapes(lib, kw, status):
     assert call(lib, "moda_tree_mask", base(**kw), 5) == status, moda.moda_last_error_message()
 
 
+@pytest.mark.parametrize("B", [2 ** 31 - 1, 2 ** 31 - 1023])
+def test_too_many_requests(lib, B):
+    """A thread's share of them is rounded up in 32 bits."""
+    sh = base(B=B, max_pages=1, Hq=1, Hk=1)
+    assert call(lib, "moda_tree_decode", sh, 12, 1 << 40) == moda.MODA_ERR_UNSUPPORTED
+    assert lib.moda_tree_decode_workspace_size(ctypes.byref(sh)) == ctypes.c_size_t(-1).value
+    assert call(lib, "moda_tree_mask", sh, 5) == moda.MODA_ERR_UNSUPPORTED
+    assert lib.moda_tree_decode_workspace_size(ctypes.byref(base(B=2 ** 28, max_pages=1, N=64))) > 0
+
+
 @pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 512, 1024])
 def test_table_length_leaves_room_for_a_tile(lib, page):
     """Positions up to a tile behind the longest request fit 32 bits."""
