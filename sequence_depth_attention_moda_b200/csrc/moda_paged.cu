@@ -544,7 +544,7 @@ moda_status check_tree(const moda_paged_shape* s, Paged* p) {
     if (s->depth_window < 0 || s->depth_window > s->L)
         return failf(MODA_ERR_INVALID_ARG, "depth_window=%lld must be in 0..L (L=%lld)", s->depth_window, s->L);
     if (!(s->softmax_scale >= 0.0f) || std::isinf(s->softmax_scale))
-        return failf(MODA_ERR_INVALID_ARG, "softmax_scale must be finite (<= 0 for 1/sqrt(d))");
+        return failf(MODA_ERR_INVALID_ARG, "softmax_scale must be >= 0 and finite (0 selects 1/sqrt(d))");
     if (static_cast<double>(s->N) * s->Hq > 2147483647.0 || static_cast<double>(s->N) * s->Hk > 2147483647.0)
         return failf(MODA_ERR_UNSUPPORTED, "N=%lld tokens of Hq=%lld heads pass 32-bit row indices", s->N, s->Hq);
     p->Hq = s->Hq; p->G = s->Hq / s->Hk; p->L = s->L;

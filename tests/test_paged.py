@@ -195,6 +195,12 @@ def test_table_length_leaves_room_for_a_tile(lib, page):
         assert lib.moda_page_plan(ctypes.byref(sh), *[FAKE + 256 * i for i in range(8)], None) == moda.MODA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("scale", [-1.0, float("inf"), float("nan")])
+def test_refused_scale_says_what_is_accepted(lib, scale):
+    assert call(lib, "moda_tree_decode", base(softmax_scale=scale), 12, 1 << 40) == moda.MODA_ERR_INVALID_ARG
+    assert ">= 0 and finite" in moda.moda_last_error_message()
+
+
 def test_null_shape_and_pointers(lib):
     for name, n in (("moda_page_plan", 8), ("moda_cache_append", 5), ("moda_tree_mask", 5)):
         assert call(lib, name, None, n) == 1
