@@ -259,30 +259,17 @@ struct Walk {
     RawRequest ahead;    // of request j.b + 1
     int i0, i1;          // this CTA's tiles of the job
     int end;             // where the CTA's part ends, from the job's beginning
-    int seg;             // 0 for the first
     __device__ __forceinline__ bool begin(const TreeArgs& a, const Start& s) {
         if (s.length == 0) return false;
         j = s.j;
         look_ahead(a);
         end = s.lo + s.length;
         take(a, tile_from(a, j, s.lo));
-        seg = 0;
         // the part may begin behind the job's last tile's beginning, or end before the
         // first one's: then it has none of this job (nor does the combine kernel look for it)
-        return i0 < i1 || next_job(a);
+        return i0 < i1 || next(a);
     }
     __device__ __forceinline__ bool next(const TreeArgs& a) {
-        ++seg;
-        return next_job(a);
-    }
-    // Whether this CTA owns the job whole (then it writes the outputs itself).
-    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == j.nt; }
-    // Where its record of a cut job goes: a job that began before the part is the
-    // part's first, one that begins in it and goes on is its last.
-    __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (i0 == 0); }
-
-   private:
-    __device__ __forceinline__ bool next_job(const TreeArgs& a) {
         end -= j.cost;
         if (end <= a.job_cost) return false;
         int g = j.group + 1;
@@ -301,6 +288,13 @@ struct Walk {
         take(a, 0);
         return true;
     }
+    // Whether this CTA owns the job whole (then it writes the outputs itself).
+    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == j.nt; }
+    // Where its record of a cut job goes: a job that began before the part is the
+    // part's first, one that begins in it and goes on is its last.
+    __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (i0 == 0); }
+
+   private:
     __device__ __forceinline__ void look_ahead(const TreeArgs& a) {
         if (j.b + 1 < a.B) ahead = load_raw(a, j.b + 1);
     }
