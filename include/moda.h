@@ -226,7 +226,9 @@ moda_status moda_bwd_noalloc(const moda_shape* shape,
  * thread records events[0] on its stream before its first kernel launch and
  * events[k] right after its k-th launch: moda_fwd has one launch; moda_bwd
  * has three (row dots D = rowsum(dO*O), the dK/dV kernel, the dQ + depth-
- * gradient kernel), so it uses events[0..3].  Markers beyond n are skipped.
+ * gradient kernel), so it uses events[0..3].  moda_decode and moda_tree_decode
+ * record events[0] before their first launch and events[1] after their last.
+ * Markers beyond n are skipped.
  *   events   array of n cudaEvent_t handles, created and owned by the caller
  *   n        0..8; 0 turns the markers off
  * Nothing is allocated; the library keeps only the handles (thread-local).

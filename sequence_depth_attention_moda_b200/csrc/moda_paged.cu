@@ -36,8 +36,9 @@ namespace {
 // threads as many short ones do.  Released pages are written before any is
 // taken, and table entries before slots read them: CTA barriers where one CTA
 // does it all, else barriers of a cluster of 8 (see launch_plan for the choice).
-// The slots of many tokens are a grid of their own.  Measured inside a graph: 256
-// requests of 8 new tokens 6.3 us, 64 prompts of up to 8192 tokens 8.6 us.
+// The slots of many tokens are a grid of their own.  Measured inside a graph, a call that
+// takes pages and the one that gives them back together: 256 requests of 8 new tokens
+// 12.9 us, 64 prompts of up to 8192 tokens 17.4 us.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxPlanRequests = 16384;
@@ -341,13 +342,18 @@ cudaError_t launch_dependent(void (*kernel)(A), dim3 grid, unsigned block, int s
 }
 
 cudaError_t launch_plan(PlanArgs& a, cudaStream_t s) {
-    // One CTA while its 1024 threads need few turns for the pages that may move (at most
+    // One CTA while its 1024 threads need few turns for the pages that may be taken (at most
     // N / page + B), else a cluster of 8; and slots in a grid of their own from where its
     // SMs gain more than the second launch costs.  Measured inside a graph, one CTA
-    // against the cluster: 256 requests, 2048 tokens (pages of 64) 5.3, 6.3 us; with the
-    // slots apart 2048 requests, 16384 tokens 8.3, 8.7; 64, 32768 (pages of 16) 7.6, 7.5;
-    // 1024, 65536 (16) 11.2, 8.8.  Slots by the plan's one CTA against apart: 4096 tokens
-    // 6.1, 6.5; 8192 7.8, 7.1; 16384 10.3, 7.0.
+    // against the cluster: 256 requests, 2048 tokens (pages of 64) 7.6, 8.4 us; with the
+    // slots apart 2048 requests, 16384 tokens 11.1, 11.3; 64, 32768 (pages of 16) 8.8, 7.9;
+    // 1024, 65536 (16) 12.8, 9.5.  Slots by the plan's one CTA against apart: 4096 tokens
+    // 8.3, 8.9; 8192 12.1, 9.6; 16384 20.0, 11.1.
+    // N does not bound the pages that are given back, and what does, B * max_pages, is large
+    // for every server: the host cannot tell a call that ends many long requests from a step
+    // that moves a few pages.  With a small N it gets the one CTA, which then is the slower
+    // choice (2048 pages given back 5.9 us against 6.5, 4096 7.4, 6.7; 8192 11.9, 6.8;
+    // 131072, 256 requests of 8192 tokens in pages of 16, 122, 22).
     const bool small = static_cast<long long>(a.N >> a.page_shift) + a.B <= 4 * kPlanThreads;
     a.slots_here = a.N <= kPlanThreads * kSlotsPerLane;
     const int list = (a.B + 1) * static_cast<int>(sizeof(int)), smem = 3 * list;
@@ -366,8 +372,8 @@ cudaError_t launch_plan(PlanArgs& a, cudaStream_t s) {
 // A copy of N rows of Hk*d elements for K and for V, 16 bytes a thread and
 // access; a head's d elements are contiguous on both sides (128 to 512 bytes).
 // Bound by HBM: every byte is read once and written once.  Measured: 32768 tokens of
-// 8 heads (268 MB moved) 43.5 us, 94% of a plain copy's bandwidth; 128 tokens 3.3 us
-// inside a graph.
+// 8 heads (268 MB moved) 43.5 us, 94% of a plain copy's bandwidth; 128 tokens 3.2 us
+// inside a graph, 6.5 to 6.9 through the Python binding.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 4;
 
@@ -424,7 +430,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
 // stores them when it leaves them behind.  A CTA has 256 tokens of a request.
 // Bound by the launch and by latency: random trees are shallow, a chain of n costs
 // its last token n steps of about 60 cycles.  Measured inside a graph: 8 requests of
-// 32 tokens 1.9 us, 256 of 256 3.6 us, 8 of 2048 13 us, a chain of 2048 73 us.
+// 32 tokens 1.5 us, 256 of 256 3.0 us (both 11 through the Python binding), 8 of 2048 13 us,
+// a chain of 2048 73 us.
 constexpr int kMaskThreads = 256;
 constexpr int kMaskGroup = 4;        // words a walk collects
 constexpr int kMaxMaskWords = 64;
@@ -623,6 +630,10 @@ TreePlan tree_plan(const Paged& p) {
         // 8192 196, 176.  n = 256 over 4096 (143 MB) 185, 191; 8192 347, 326.  n = 1000 over
         // 4096 (167 MB) 818, 789.  With d = 64 a tile's bytes are half and its exponentials
         // the same: n = 64 over 32768 257, 272.
+        // The lengths are on the device: what counts here is the pool and the table, and all N
+        // rows.  Where those are much larger than what the requests hold, two tiles are taken
+        // for short requests too (n = 64 over 4096 keys: 75 us in a pool of 4 GB and a table of
+        // 128K tokens, 65 in a tight one; n = 128 123, 113).
         const double pages = double(p.B) * p.max_pages < p.n_pages ? double(p.B) * p.max_pages : p.n_pages;
         const double cache = pages * p.page * p.Hk * p.d * 2 * p.elem_bytes;
         t.tiles = per > t.Tq && p.d == 128 && cache > (per > 2 * t.Tq ? 160e6 : 280e6) ? 2 : 1;
@@ -632,7 +643,9 @@ TreePlan tree_plan(const Paged& p) {
         t.KT = 32;
         const long long rows = static_cast<long long>(per) * p.G;     // of a request and KV head
         // (a block of more rows than there are costs their arithmetic: 8 requests, G = 4, d = 128,
-        // T = 8192: n = 1 in blocks of 4, 16, 64 rows 143, 228, 524 us; n = 4 in 16, 64 232, 526)
+        // T = 8192: n = 1 in blocks of 4, 16, 64 rows 143, 228, 524 us; n = 4 in 16, 64 232, 526.
+        // N counts padding rows: 8 requests of one token padded to 64 rows take blocks of 64,
+        // 269 us: warps without a row skip the work)
         t.rows = p.G <= 4 && rows <= 4 ? 4 : (p.G <= 16 && rows <= 16 ? 16 : 64);
         t.Tq = t.rows / p.G;
         t.Lp = Lw;

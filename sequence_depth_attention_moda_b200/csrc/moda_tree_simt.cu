@@ -19,11 +19,11 @@
 // that holds a request's rows on average: padded rows cost as much arithmetic as
 // real ones.  Shared memory rows are padded by 16 bytes, and the lanes are laid out
 // so that the eight of a quarter warp read different banks (with the lanes that
-// share a block always adjacent, R = 64 took 680 us where it now takes 533).
+// share a block always adjacent, R = 64 took 680 us where it then took 533).
 //
-// Measured (8 requests, 32 query heads over 8, d 128, 8192 keys each): 1 token
-// 142 us (R = 4; keys and values of 0.54 GB at 3.8 TB/s), 4 tokens 237 (R = 16),
-// 16 tokens 523 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
+// Measured inside a graph (8 requests, 32 query heads over 8, d 128, 8192 keys each): 1
+// token 139 us (R = 4; keys and values of 0.54 GB at 3.9 TB/s), 4 tokens 235 (R = 16),
+// 16 tokens 517 (R = 64; 17 GFLOP, half of what the FMA pipes can do: shared memory
 // reads 8 vectors for 64 multiply-adds, and larger blocks do not fit the registers of
 // two CTAs an SM).  One tile in flight and plain loads: 359, 363 and 743 us.
 #include "moda_tree.cuh"
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(const __grid_con
             }
             // Whether any of the warp's rows sees any of the tile's: not those behind the last
             // token, nor, in a depth tile, other tokens' rows (their p will be 0).  22 requests of
-            // up to 78 tokens over 221 keys: 103 us without, 97 with.
+            // up to 78 tokens over 221 keys: 103 us without, 97 with it.
             bool mine = true;
             if (R > 4 && wr0 >= rows) mine = false;
             if (R > 4 && dep) {

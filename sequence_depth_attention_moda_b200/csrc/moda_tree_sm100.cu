@@ -35,12 +35,14 @@
 // segment (add_not_finite).  Tiles of held keys pass untouched.
 //
 // Measured (32 query heads over 8, d 128, 48 depth rows, 8 requests of 32768 keys):
-// 1 token 172 us, 6.2 TB/s, where the bytes alone take 164; 32 tokens 201 to 205, and
-// 225 once the power cap has brought the clock to 1.4 GHz: a tile's block then takes
-// the softmax warps as long as HBM its bytes.  A block takes about 2000 cycles, of
+// 1 token 168 to 174 us inside a graph, 6.2 TB/s, where the bytes alone take 164, and 181
+// to 186 among calls on changing inputs through the Python binding; 32 tokens 190 to 205,
+// and 224 to 230 once the power cap has brought the clock to 1.4 GHz: a tile's block then
+// takes the softmax warps as long as HBM its bytes.  A block takes about 2000 cycles, of
 // which 1024 are exponentials (16 a cycle) and 1024 tensor work; the rest is latency
 // of two warps a sub-partition.  48 ragged requests of up to 64 tokens over 4096 keys
-// 85 us (the bytes 41), 11 of them before the first block.
+// 82 to 89 us inside a graph, 92 on changing inputs (the bytes 41), 11 of them before the
+// first block.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -216,8 +218,7 @@ __device__ __forceinline__ Box tile_box(const TreeArgs& a, int box_rows, int sla
 // Rows r0 .. r0+15 of a V stage (whole warp): clears those that P V covers but
 // that are not there (from `rows` on; of every `pitch` rows those behind the
 // first `used`), and takes infinities and NaN out of those from row `from` on,
-// which are masked for some query row.  True if it found any.  A call of its
-// own, so that its registers are not the tile loop's.
+// which are masked for some query row.  True if it found any.
 template <int D>
 __device__ __forceinline__ bool clean_values(unsigned char* stage, int r0, int rows, int from, int pitch, int used) {
     const int lane = threadIdx.x & 31;
@@ -278,8 +279,8 @@ __device__ __forceinline__ bool clean_values(unsigned char* stage, int r0, int r
     return bad;
 }
 
-// mask_visible of 64 keys.  (A call, like clean_values; its arguments are values,
-// since a reference to the kernel's parameters is read through global memory.)
+// mask_visible of 64 keys.  (Its arguments are values: a reference to the kernel's
+// parameters was read through memory.)
 __device__ __forceinline__ uint2 mask_visible64(const uint32_t* row, int words, int n, int rel) {
     return make_uint2(mask_visible(row, words, n, rel), mask_visible(row, words, n, rel + 32));
 }
