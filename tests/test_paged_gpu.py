@@ -1,6 +1,7 @@
 """The paged calls on the GPU against the oracle: page plans, appends, tree
 masks, the attention of drafted tokens, and a run of them together."""
 import dataclasses
+import threading
 
 import numpy as np
 import pytest
@@ -812,6 +813,123 @@ def test_step_captured_over_two_streams():
     torch.cuda.synchronize()
     assert pos.tolist() == pos_ref.tolist()
     check_tree(c, x, see, o, lse)
+
+
+def test_tree_from_several_threads():
+    """Calls of four host threads, each on its own stream with its own buffers."""
+    cases = [Tree(held=(900, 70), new=(9, 30), L=4), Tree(held=(50,) * 30, new=(3,) * 30, L=2, seed=2),
+             Tree(held=(300,), new=(70,), Hq=4, Hk=2, d=64, L=1, chain=True), Tree(held=(20, 400), new=(5, 8), dtype="fp32")]
+    made = [make_tree(c) for c in cases]
+    todo = [(c, x, see, sh, to_device(x)) for c, (x, see, sh) in zip(cases, made)]
+    torch.cuda.synchronize()
+    errors, outs = [], [None] * len(todo)
+
+    def work(i):
+        try:
+            c, x, see, sh, y = todo[i]
+            s = torch.cuda.Stream()
+            n = moda.moda_tree_decode_workspace_size(sh)
+            with torch.cuda.stream(s):
+                ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+                for _ in range(60):
+                    o, lse = torch.full_like(y["q"], float("nan")), torch.full(y["q"].shape[:2], float("nan"), device=DEV)
+                    moda.moda_tree_decode(sh, y["q"], y["kc"], y["vc"], y["Kd"], y["Vd"], y["table"], y["held"], y["cu"], y["mask"],
+                                          o, lse, ws, n)
+            s.synchronize()
+            outs[i] = o, lse
+        except Exception as e:      # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(todo))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for (c, x, see, _, _), (o, lse) in zip(todo, outs):
+        check_tree(c, x, see, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tree_no_new_tokens(dtype):
+    """Requests without new tokens and rows that belong to none: nothing is written."""
+    c = Tree(held=(40, 0, 900), new=(0, 0, 0), L=2, pad=5, dtype=dtype)
+    x, see, sh = make_tree(c)
+    o, lse = run_tree(to_device(x), sh)
+    assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_steps_back_to_back(dtype):
+    """Steps that move pages, one behind the other in a graph, each kernel set up while
+    the one before runs: the bits of the same calls with a wait after each."""
+    rng = np.random.default_rng(5)
+    g = torch.Generator().manual_seed(5)
+    dt = torch_dtype(dtype)
+    B, Hq, Hk, d, L, P, n_pages, mp = 40, 8, 2, 64, 2, 8, 900, 20
+    N = 3 * B
+    sh = moda.make_paged_shape(B, N, Hq, Hk, d, L, P, n_pages, mp, 1, moda.MODA_FP32 if dtype == "fp32" else 0)
+    nws = moda.moda_tree_decode_workspace_size(sh)
+    ws = torch.empty(nws, dtype=torch.uint8, device=DEV)
+    state0 = dict(kc=torch.randn(n_pages, Hk, P, d, generator=g).to(dt), vc=torch.randn(n_pages, Hk, P, d, generator=g).to(dt),
+                  table=torch.full((B, mp), -1, dtype=torch.int32), free=torch.randperm(n_pages, generator=g).to(torch.int32),
+                  count=torch.tensor([n_pages], dtype=torch.int32))
+    state = to_device(state0)
+    held, steps = rng.integers(0, 120, B), []
+    big = moda.make_paged_shape(B, int(held.sum()), Hq, Hk, d, L, P, n_pages, mp)
+    moda.moda_page_plan(big, dev_i32([0] * B), dev_i32(held), state["table"], state["free"], state["count"], dev_i32([0] * (B + 1)),
+                        dev_i32([0] * B), torch.zeros(big.N, dtype=torch.int64, device=DEV))
+    state0 = {n: t.clone() for n, t in state.items()}
+    for _ in range(8):       # lengths wander up and down
+        back = np.where(rng.random(B) < 0.3, rng.integers(0, held + 1), held)
+        want = np.minimum(back + rng.integers(0, 4, B), mp * P)
+        steps.append(dict(held=dev_i32(held), back=dev_i32(back), want=dev_i32(want),
+                          parent=dev_i32(np.full(N, -1)), q=torch.randn(N, Hq, d, generator=g).to(dt).to(DEV),
+                          k=torch.randn(N, Hk, d, generator=g).to(dt).to(DEV), v=torch.randn(N, Hk, d, generator=g).to(dt).to(DEV),
+                          kd=torch.randn(N, Hk, L, d, generator=g).to(dt).to(DEV), vd=torch.randn(N, Hk, L, d, generator=g).to(dt).to(DEV)))
+        held = want
+    for s in steps:
+        for n, shape, t in (("cu", (B + 1,), torch.int32), ("cu2", (B + 1,), torch.int32), ("granted", (B,), torch.int32),
+                            ("granted2", (B,), torch.int32), ("slots", (N,), torch.int64), ("mask", (N, 1), torch.int32),
+                            ("pos", (N,), torch.int32), ("o", (N, Hq, d), dt), ("lse", (N, Hq), torch.float32)):
+            s[n] = torch.zeros(shape, dtype=t, device=DEV)
+
+    def run(wait):
+        y = state
+        for s in steps:
+            for call in (
+                lambda: moda.moda_page_plan(sh, s["held"], s["back"], y["table"], y["free"], y["count"], s["cu2"], s["granted2"], s["slots"]),
+                lambda: moda.moda_page_plan(sh, s["back"], s["want"], y["table"], y["free"], y["count"], s["cu"], s["granted"], s["slots"]),
+                lambda: moda.moda_cache_append(sh, s["k"], s["v"], s["slots"], y["kc"], y["vc"]),
+                lambda: moda.moda_tree_mask(sh, s["parent"], s["cu"], s["back"], s["mask"], s["pos"]),
+                lambda: moda.moda_tree_decode(sh, s["q"], y["kc"], y["vc"], s["kd"], s["vd"], y["table"], s["back"], s["cu"], s["mask"],
+                                              s["o"], s["lse"], ws, nws),
+            ):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+
+    names = ("granted", "slots", "mask", "pos", "o", "lse")
+    run(True)
+    moda.moda_check_status()
+    ref = [{n: s[n].clone() for n in names} for s in steps]
+    end = {n: t.clone() for n, t in state.items()}
+    assert all(torch.equal(s["granted"], s["want"]) for s in steps) and int(end["count"]) < n_pages - 2 * B
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(False)
+    for _ in range(10):
+        for n, t in state.items():
+            t.copy_(state0[n])
+        for s in steps:
+            for n in names:
+                s[n].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, r in zip(steps, ref):
+            for n in names:
+                assert torch.equal(s[n], r[n]), n
+        assert all(torch.equal(state[n], end[n]) for n in state)
 
 
 # ------------------------------------------------------------------- together --
