@@ -144,8 +144,10 @@ __device__ __forceinline__ void write_slots(const PlanArgs& a, const int* s_cu, 
             const int held = static_cast<int>(min(static_cast<long long>(max(a.held[b], 0)), cap));
             const int key = held + static_cast<int>(t - s_cu[b]);
             const int page = __ldcg(a.table + static_cast<size_t>(b) * a.max_pages + (key >> a.page_shift));
-            if (is_page(a, page)) slot[u] = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-            else atomicOr(a.status, kStatusBadIndex);
+            if (is_page(a, page))
+                slot[u] = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            else
+                atomicOr(a.status, kStatusBadIndex);
         }
     }
 #pragma unroll
@@ -185,7 +187,9 @@ __device__ __noinline__ void pack_released(const PlanArgs& a, const int* s_drop,
     long long place = count;
     for (long long i0 = 0; i0 < drops; i0 += kPlanThreads) {
         const long long i = i0 + threadIdx.x;
-        int* entry = i >= drops ? nullptr : (listed ? a.free_pages + count + i : released_entry(a, s_drop, static_cast<unsigned>(drops - 1 - i)));
+        int* entry = nullptr;
+        if (i < drops)
+            entry = listed ? a.free_pages + count + i : released_entry(a, s_drop, static_cast<unsigned>(drops - 1 - i));
         const int page = entry ? __ldcg(entry) : -1;
         long long at = is_page(a, page), none = 0, n, n_none;
         block_prefix(at, none, warp_sum, &n, &n_none);       // (all have read before any writes)

@@ -17,11 +17,11 @@
 // between two of a job's tiles has one of them itself).  Lengths live on the
 // device (a captured graph replays with other ones), so every CTA adds up the
 // list itself.  Where cu_new descends the requests share rows and the host's bound
-// does not hold: then the list is empty.  A job that one CTA owns whole is written out by it; of a job
-// cut at a range's end every CTA leaves one (m, l, o) record a row, and the
-// combine kernel merges them in CTA order.  At most two of a CTA's jobs can be
-// cut (its first and its last), so the records take 2 slots a CTA whatever
-// the lengths.
+// does not hold: then the list is empty.  A job that one CTA owns whole is
+// written out by it; of a job cut at a range's end every CTA leaves one (m, l, o)
+// record a row, and the combine kernel merges them in CTA order.  At most two of
+// a CTA's jobs can be cut (its first and its last), so the records take 2 slots a
+// CTA whatever the lengths.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -368,10 +368,10 @@ __device__ __forceinline__ int page_of(const TreeArgs& a, int b, int key) {
 //
 // A warp goes once over the keys and depth rows that any of its rows sees, whole rows
 // of V at a time, and notes for each column which of its rows see a +Inf and which a
-// -Inf (a NaN counts as both): the time is that of reading V.  A chain of
-// 4096 tokens with an infinity or NaN in three of 8 heads' values (32 query heads, d = 128):
-// 2.2 ms against 0.30 without, in fp32 6.5 against 4.4.  A walk over the keys for every
-// column of every row took 560 and 950 ms.
+// -Inf (a NaN counts as both): the time is that of reading V.  A chain of 4096 tokens
+// with an infinity or NaN in three of 8 heads' values (32 query heads, d = 128): 2.3 ms
+// against 0.30 without, in fp32 6.4 against 4.3.  A walk over the keys for every column
+// of every row took 560 and 950 ms.
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
@@ -379,10 +379,11 @@ __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __f
 
 // Rows row0, row0 + step, ... (n <= 16 of them; row = token * G + head, from the
 // request's token tok0 on) of a KV head's outputs, which the warp's lanes stored before
-// (or others, and a barrier).  Whole warp.  kAhead: rows of V in flight, which bound the time and the
-// registers (a callee's count is its kernel's too).
+// (or others, and a barrier).  Whole warp.  kAhead: rows of V in flight, which bound the
+// time and the registers (a callee's count is its kernel's too).
 template <typename E, int D, int kAhead>
-__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Request r, int b, int hk, int tok0, int row0, int step, int n) {
+__device__ __noinline__ void add_not_finite(const TreeArgs& a, const Request r, int b, int hk, int tok0, int row0,
+                                            int step, int n) {
     constexpr int C = D / 32;            // columns C * lane .. of a row are the lane's
     constexpr int kWords = C * static_cast<int>(sizeof(E)) / 4;
     constexpr uint32_t kAll = 0xffffffffu;
