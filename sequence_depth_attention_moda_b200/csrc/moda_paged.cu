@@ -38,7 +38,7 @@ namespace {
 // does it all, else barriers of a cluster of 8 (see launch_plan for the choice).
 // The slots of many tokens are a grid of their own.  Measured inside a graph, a call that
 // takes pages and the one that gives them back together: 256 requests of 8 new tokens
-// 12.9 us, 64 prompts of up to 8192 tokens 17.4 us.
+// 12.7 us, 64 prompts of up to 8192 tokens 17.0 us.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxPlanRequests = 16384;
@@ -54,10 +54,16 @@ struct PlanArgs {
     int slots_here;                  // the plan kernel writes the slots itself
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 template <int CTAS>
 __device__ __forceinline__ void plan_barrier() {
-    if (CTAS == 1) __syncthreads();
-    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (CTAS == 1) {
+        __syncthreads();
+    } else {
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Exclusive prefixes of x and y over the CTA's threads; tx and ty get the sums.
@@ -157,21 +163,20 @@ __device__ __forceinline__ void write_slots(const PlanArgs& a, const int* s_cu, 
     }
 }
 
-// The sum over the grid of each CTA's *x, which is in shared memory, behind a barrier.
+// Adds n to *x in the shared memory of every CTA.  (Rare, where a sum read from the
+// others costs every call 0.7 us.)
 template <int CTAS>
-__device__ __forceinline__ int grid_sum(const int* x) {
-    plan_barrier<CTAS>();
-    if (CTAS == 1) return *x;
-    int sum = 0;
-#pragma unroll
+__device__ __forceinline__ void add_everywhere(int* x, int n) {
+    if (CTAS == 1) {
+        atomicAdd(x, n);
+        return;
+    }
+#pragma unroll 1
     for (int r = 0; r < CTAS; ++r) {
         uint32_t at;
-        int y;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(x)), "r"(r));
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
-        sum += y;
+        asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(at), "r"(n) : "memory");
     }
-    return sum;
 }
 
 // The table's entry for released page x of the call; s_drop: prefixes of those pages.
@@ -213,6 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     const int ch = (a.B + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(a.B, tid * ch), b1 = min(a.B, b0 + ch);
     if (tid == 0) s_lost = 0;
+    if (CTAS > 1) cluster_arrive();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
@@ -226,6 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         drop += max(r.have - r.need, 0);
     }
     block_prefix(take, drop, warp_sum, &takes, &drops);
+    if (CTAS > 1) cluster_wait();        // every CTA has begun, with its s_lost at 0
     // released pages onto the list
     const int count = min(max(count0, 0), a.n_pages);
     const bool room = count + drops <= a.n_pages;      // else some of them cannot be pages, or the list is wrong
@@ -246,8 +253,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
             a.free_pages[count + static_cast<int>(drops) - 1 - static_cast<int>(x)] = page;
             *entry = -1;
         }
-        if (mine > 0) atomicAdd(&s_lost, mine);
-        lost = grid_sum<CTAS>(&s_lost);
+        if (mine > 0) add_everywhere<CTAS>(&s_lost, mine);
+        plan_barrier<CTAS>();
+        lost = s_lost;
         if (lost > 0 || !room) {         // (rare) one CTA moves the pages together, from the list's bottom
             if (rank == 0) pack_released(a, s_drop, warp_sum, count, drops, room);
             plan_barrier<CTAS>();
@@ -305,8 +313,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         a.table[static_cast<size_t>(b) * a.max_pages + plan_request(a, b).have + (static_cast<int>(x) - s_take[b])] = page;
     }
     if (rank == 0 && tid == 0) *a.free_count = static_cast<int>(min(top - granted, static_cast<long long>(a.n_pages)));
-    if (a.slots_here || (CTAS > 1 && drops > 0)) plan_barrier<CTAS>();   // (or: until grid_sum's reads are done)
     if (!a.slots_here) return;
+    plan_barrier<CTAS>();
     for (long long t0 = (all >> 5) * 32ll * kSlotsPerLane; t0 < a.N; t0 += CTAS * kPlanThreads * kSlotsPerLane)
         write_slots(a, s_cu, t0, lane);
 }
